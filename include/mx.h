@@ -296,6 +296,136 @@ int mx_qsnr(int dtype, const void *ref, const void *approx, int64_t n,
 int mx_gemm(const mx_format *fa, const mx_qtensor *a, const mx_format *fb,
             const mx_qtensor *b, void *c, int64_t ldc, int c_dtype, void *stream);
 
+/* ---- one decode step with quantized weights and a quantized cache ----------
+ * The entry points below serve new tokens with weights and a key-value cache
+ * in this library's formats: the product of a few unquantized tokens with a
+ * 4-bit weight, the norm and rotation of query and key heads (with its
+ * gradient, for training), the write of new keys and values to a paged cache,
+ * and the attention of one new token per sequence over that cache.           */
+
+/* y = x . deq(W)^T + bias for a few tokens: x is tokens x w->cols (row stride
+ * ldx elements, dtype x_dtype), W a quantized tensor of w->rows x w->cols, y
+ * tokens x w->rows (row stride ldy, y_dtype, rounded to nearest even from the
+ * fp32 sum), bias (nullable) w->rows values of x_dtype.
+ *  - Formats: E2M1 or INT4 elements in row blocks 1 x b of 8 .. 256 elements
+ *    under E8M0 (any rule), UE4M3, NVFP4 or UE5M3 scales, macro-block scales
+ *    included, symmetric or asymmetric.  How the codes were rounded does not
+ *    matter.  Anything else (other elements, E3M0 scales, rotation, column or
+ *    2D blocks): MX_ERR_UNSUPPORTED.
+ *  - W's values enter exactly (decoded to bf16, which holds every code times
+ *    its scale, down to bf16's own smallest values), an fp32 x as the exact
+ *    sum of three bf16 parts; products are summed in fp32 in a fixed order.
+ *    An offset or the INT4 bias enters as offset times the block's sum of x.
+ *  - A NaN scale code makes its row's outputs NaN, a NaN or Inf in a token
+ *    makes that token's outputs non-finite, other tokens are untouched.
+ *  - Any number of tokens runs; the kernel is made for up to 16 (more read the
+ *    weight once per 16).  w->rows < 2^31, 0 < w->cols < 2^27, tokens < 2^20.
+ *  - x, W's buffers, bias and y 16-byte aligned, ldx a multiple of 16 bytes
+ *    (MX_ERR_ALIGN).  y must not overlap an input.                           */
+int mx_matvec(const mx_format *fw, const mx_qtensor *w, int x_dtype, const void *x, int64_t tokens,
+              int64_t ldx, const void *bias, void *y, int64_t ldy, int y_dtype, void *stream);
+
+/* A set of heads: tokens x heads vectors of one dimension (given with it),
+ * the vector contiguous, strides in elements.  Strides times the element size
+ * are multiples of 16 bytes, and so is x (MX_ERR_ALIGN).  Outputs must not
+ * hold one address twice.                                                    */
+typedef struct mx_heads {
+    void *x;
+    int64_t token_stride, head_stride;
+    int32_t heads, dtype;
+} mx_heads;
+
+/* What mx_qk_rope does to each head vector x of `dim` values (a multiple of
+ * 8, at most 1024): with a weight w, n = x (mean(x^2) + eps)^-1/2 and u = w n;
+ * without one (NULL) u = x.  Then the first rot_dim values (even, 0 .. dim)
+ * are rotated in pairs by the angles of the token's position p:
+ *   y_a = u_a cos - u_b sin,  y_b = u_b cos + u_a sin
+ * with (a, b) = (i, i + rot_dim/2), or (2i, 2i + 1) when `interleaved`, and
+ * cos, sin at [p][i] of two tables of table_rows x rot_dim/2 fp32 values.  A
+ * position outside the table makes that token's rotated values NaN (all of
+ * its gradients through a norm).  tokens x heads < 2^31.  Everything
+ * between load and store is fp32.  q_weight and k_weight have w_dtype.       */
+typedef struct mx_rope {
+    int64_t tokens;
+    int32_t dim, rot_dim, interleaved, w_dtype;
+    const void *q_weight, *k_weight;
+    const float *cos, *sin;
+    int64_t table_rows;
+    const int32_t *positions;
+    float eps;
+} mx_rope;
+
+/* Norm and rotation of query and key heads, one pass over both: q_out and
+ * k_out have the inputs' heads and dtype and may be the inputs themselves
+ * (same strides), else must not overlap them.  k and k_out may be NULL
+ * (queries only).                                                            */
+int mx_qk_rope(const mx_rope *r, const mx_heads *q, const mx_heads *k, const mx_heads *q_out,
+               const mx_heads *k_out, void *stream);
+
+/* Its gradient.  dy_q, dy_k: the gradients of its outputs; q, k: its inputs;
+ * dq, dk: the gradients of its inputs (may be dy_q, dy_k themselves, same
+ * strides); dq_weight, dk_weight: fp32, dim values each, required where the
+ * weight is set (NULL otherwise), overwritten.  With g the dy rotated back,
+ * dw = sum g n over tokens and heads, and dx = rstd (w g - n mean(n w g)).
+ * The weight sums are formed in fp32 in a fixed order.  workspace: at least
+ * mx_qk_rope_workspace_size(r) bytes where a weight is set; no initial
+ * contents needed; calls that share one must not overlap.  k, dy_k and dk may
+ * be NULL together.  All heads have one dtype.                               */
+size_t mx_qk_rope_workspace_size(const mx_rope *r);
+int mx_qk_rope_backward(const mx_rope *r, const mx_heads *dy_q, const mx_heads *dy_k, const mx_heads *q,
+                        const mx_heads *k, const mx_heads *dq, const mx_heads *dk, float *dq_weight,
+                        float *dk_weight, void *workspace, size_t ws_bytes, void *stream);
+
+/* A paged cache of keys and values: `pages` pages of page_size tokens for
+ * `heads` heads of `dim` values (64, 96, 128, 192 or 256).  k and v:
+ * [page][head][token][dim] values in bf16 (format NULL), or codes as
+ * mx_quantize lays out rows of dim elements (MXFP8 E4M3: dim bytes, MXFP4:
+ * dim / 2) with k_scales and v_scales [page][head][token][dim / 32] E8M0
+ * bytes.  format: E4M3 or E2M1 elements, E8M0 scales (any rule) on 1 x 32
+ * blocks, to nearest, symmetric, not rotated (MX_ERR_UNSUPPORTED otherwise).
+ * The struct is host memory.  page_size 1 .. 65536, pages * page_size < 2^40. */
+typedef struct mx_kv_cache {
+    const mx_format *format;
+    void *k, *v, *k_scales, *v_scales;
+    int64_t pages;
+    int32_t page_size, heads, dim;
+} mx_kv_cache;
+
+/* Writes the keys and values of `tokens` new tokens to the cache.  k and v:
+ * cache->heads heads of cache->dim values each, one dtype (fp32 inputs are
+ * rounded to nearest even for a bf16 cache).  slots (device): token i goes to
+ * page slots[i] / page_size at slots[i] % page_size; a slot outside the cache
+ * (negative, or past its end) skips the token.  Codes and scales are those
+ * mx_quantize writes for the same values.  Two tokens of one slot in one call
+ * leave either's values.  tokens x heads < 2^30.                             */
+int mx_cache_write(const mx_kv_cache *cache, const mx_heads *k, const mx_heads *v, int64_t tokens,
+                   const int64_t *slots, void *stream);
+
+/* Attention of one new token per sequence: for sequence b and query head h
+ *   out[b][h] = sum_t p_t v_t,  p = softmax over t < lengths[b] of
+ *   scale * (q[b][h] . k_t),  lse[b][h] = log sum_t exp(scale q.k_t)
+ * over the tokens that page_table[b][t / page_size] and t % page_size name in
+ * the cache, of key-value head h / (q->heads / cache->heads).  q and out:
+ * `batch` tokens of q->heads heads (a multiple of cache->heads), one dtype;
+ * lse nullable, fp32, batch x q->heads dense.  page_table: batch rows of
+ * table_cols int32 pages, row stride table_stride; lengths: int32.
+ *  - lengths[b] <= 0 leaves an empty row: out 0, lse -inf.  A length past the
+ *    table (table_cols * page_size) counts as that.  What lies in the cache
+ *    at and past a length is not used, whatever it holds.  A page number
+ *    outside the cache makes its sequence's outputs NaN.
+ *  - Scores, softmax statistics and sums are fp32.  A bf16 q multiplies the
+ *    cache's exact values; fp32 q enters as the exact sum of three bf16 parts.
+ *    Probabilities enter the second product as two bf16 parts (16 bits; three
+ *    parts for fp32), their sum in fp32.
+ *  - The length is split over workgroups, their parts joined in a fixed order;
+ *    the same inputs give the same bits.  workspace: at least
+ *    mx_attend_workspace_size bytes; no initial contents needed; calls that
+ *    share one must not overlap.  table_cols * page_size < 2^30.             */
+size_t mx_attend_workspace_size(const mx_kv_cache *cache, int64_t batch, int32_t q_heads, int64_t table_cols);
+int mx_attend(const mx_kv_cache *cache, const mx_heads *q, int64_t batch, const int32_t *page_table,
+              int64_t table_cols, int64_t table_stride, const int32_t *lengths, float scale,
+              const mx_heads *out, float *lse, void *workspace, size_t ws_bytes, void *stream);
+
 /* Text for a status code (static storage). */
 const char *mx_status_string(int status);
 

@@ -34,7 +34,9 @@ ROUND_RTNE, ROUND_SR, ROUND_CEIL = range(3)
 DTYPE_F32, DTYPE_BF16 = range(2)
 
 EXPORTS = ["mx_query_sizes", "mx_quantize", "mx_quantize_noalloc", "mx_quantize_many", "mx_dequantize",
-           "mx_qsnr_workspace_size", "mx_qsnr", "mx_gemm", "mx_status_string"]
+           "mx_qsnr_workspace_size", "mx_qsnr", "mx_gemm", "mx_matvec", "mx_qk_rope",
+           "mx_qk_rope_workspace_size", "mx_qk_rope_backward", "mx_cache_write", "mx_attend_workspace_size",
+           "mx_attend", "mx_status_string"]
 
 
 class MxFormat(ctypes.Structure):
@@ -72,6 +74,24 @@ class MxSizes(ctypes.Structure):
                 ("workspace", ctypes.c_size_t)]
 
 
+class MxHeads(ctypes.Structure):
+    _fields_ = [("x", ctypes.c_void_p), ("token_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64),
+                ("heads", ctypes.c_int32), ("dtype", ctypes.c_int32)]
+
+
+class MxRope(ctypes.Structure):
+    _fields_ = [("tokens", ctypes.c_int64), ("dim", ctypes.c_int32), ("rot_dim", ctypes.c_int32),
+                ("interleaved", ctypes.c_int32), ("w_dtype", ctypes.c_int32), ("q_weight", ctypes.c_void_p),
+                ("k_weight", ctypes.c_void_p), ("cos", ctypes.c_void_p), ("sin", ctypes.c_void_p),
+                ("table_rows", ctypes.c_int64), ("positions", ctypes.c_void_p), ("eps", ctypes.c_float)]
+
+
+class MxKVCache(ctypes.Structure):
+    _fields_ = [("format", ctypes.POINTER(MxFormat)), ("k", ctypes.c_void_p), ("v", ctypes.c_void_p),
+                ("k_scales", ctypes.c_void_p), ("v_scales", ctypes.c_void_p), ("pages", ctypes.c_int64),
+                ("page_size", ctypes.c_int32), ("heads", ctypes.c_int32), ("dim", ctypes.c_int32)]
+
+
 class MxError(RuntimeError):
     def __init__(self, status, where):
         self.status = status
@@ -102,10 +122,22 @@ def lib():
         L.mx_qsnr.argtypes = [i32, vp, vp, i64, P(MxStats), P(ctypes.c_double), vp,
                               ctypes.c_size_t, vp]
         L.mx_gemm.argtypes = [P(MxFormat), P(MxQTensor), P(MxFormat), P(MxQTensor), vp, i64, i32, vp]
+        sz = ctypes.c_size_t
+        L.mx_matvec.argtypes = [P(MxFormat), P(MxQTensor), i32, vp, i64, i64, vp, vp, i64, i32, vp]
+        H = P(MxHeads)
+        L.mx_qk_rope.argtypes = [P(MxRope), H, H, H, H, vp]
+        L.mx_qk_rope_workspace_size.argtypes = [P(MxRope)]
+        L.mx_qk_rope_workspace_size.restype = sz
+        L.mx_qk_rope_backward.argtypes = [P(MxRope), H, H, H, H, H, H, vp, vp, vp, sz, vp]
+        L.mx_cache_write.argtypes = [P(MxKVCache), H, H, i64, vp, vp]
+        L.mx_attend_workspace_size.argtypes = [P(MxKVCache), i64, ctypes.c_int32, i64]
+        L.mx_attend_workspace_size.restype = sz
+        L.mx_attend.argtypes = [P(MxKVCache), H, i64, vp, i64, i64, vp, ctypes.c_float, H, vp, vp, sz, vp]
         L.mx_status_string.argtypes = [i32]
         L.mx_status_string.restype = ctypes.c_char_p
         for name in ("mx_query_sizes", "mx_quantize", "mx_quantize_noalloc", "mx_quantize_many",
-                     "mx_dequantize", "mx_qsnr", "mx_gemm"):
+                     "mx_dequantize", "mx_qsnr", "mx_gemm", "mx_matvec", "mx_qk_rope", "mx_qk_rope_backward",
+                     "mx_cache_write", "mx_attend"):
             getattr(L, name).restype = ctypes.c_int
         _lib = L
     return _lib
@@ -354,3 +386,251 @@ def mx_gemm(fa: Format, a: QTensor, fb: Format, b: QTensor, c=None, out_dtype=to
                        _dtype_code(c), _stream(stream))
     _check(rc, "mx_gemm")
     return c
+
+
+# ---- one decode step with quantized weights and a quantized cache ------------
+# These calls are small enough that the host's share counts: arguments are
+# packed with as few steps as their checks allow.
+_DTYPES = {torch.float32: DTYPE_F32, torch.bfloat16: DTYPE_BF16}
+
+
+def _code(dtype):
+    try:
+        return _DTYPES[dtype]
+    except KeyError:
+        raise TypeError(f"unsupported dtype {dtype}") from None
+
+
+def _stream_ptr(stream):
+    return torch.cuda.current_stream().cuda_stream if stream is None else stream.cuda_stream
+
+
+def _raw(t):
+    return None if t is None else t.data_ptr()
+
+
+def _need(cond, what):
+    if not cond:
+        raise ValueError(what)
+
+
+def _heads(t, dim, device, what):
+    """An mx_heads of a tokens x heads x dim tensor whose last dimension is contiguous."""
+    if t.dim() != 3 or t.shape[2] != dim or t.stride(2) != 1 or t.device != device:
+        raise ValueError(f"{what}: expected tokens x heads x {dim} on {device}, the last dimension contiguous")
+    st = t.stride()
+    return MxHeads(t.data_ptr(), st[0], st[1], t.shape[1], _code(t.dtype))
+
+
+def mx_matvec(fmt: Format, w: QTensor, x: torch.Tensor, bias=None, y=None, out_dtype=None, stream=None):
+    """y = x . deq(W)^T + bias for a few unquantized tokens x (tokens x K, bf16
+    or fp32, any row stride) and a 4-bit weight W (N x K: E2M1 or INT4 in row
+    blocks, see include/mx.h).  bias: None or N values of x's dtype.  y: a
+    tokens x N view to write into, else a new tensor of out_dtype (default: x's)."""
+    _need(x.dim() == 2 and x.shape[1] == w.cols and x.device == w.codes.device and (x.shape[0] == 0 or x.stride(1) == 1),
+          f"mx_matvec: x must be tokens x {w.cols} with contiguous rows on the weight's device")
+    tokens = x.shape[0]
+    xd = _code(x.dtype)
+    if bias is not None:
+        _need(bias.shape == (w.rows,) and bias.dtype == x.dtype and bias.is_contiguous() and bias.device == x.device,
+              f"mx_matvec: bias must be {w.rows} contiguous values of x's dtype")
+    if y is None:
+        y = torch.empty((tokens, w.rows), dtype=x.dtype if out_dtype is None else out_dtype, device=x.device)
+    else:
+        _need(y.shape == (tokens, w.rows) and (y.numel() == 0 or y.stride(1) == 1) and y.device == x.device,
+              f"mx_matvec: y must be {tokens} x {w.rows} with contiguous rows")
+    one = tokens <= 1
+    rc = lib().mx_matvec(ctypes.byref(fmt.c()), ctypes.byref(w.c()), xd, x.data_ptr(), tokens,
+                         w.cols if one else x.stride(0), _raw(bias), y.data_ptr(), w.rows if one else y.stride(0),
+                         _code(y.dtype), _stream_ptr(stream))
+    _check(rc, "mx_matvec")
+    return y
+
+
+def _rope_args(q, k, cos, sin, positions, q_weight, k_weight, eps, interleaved, where):
+    """The mx_rope of a call, its shapes checked."""
+    tokens, _, dim = q.shape
+    rot = 2 * cos.shape[1]
+    dev = q.device
+    for t in (cos, sin):
+        _need(t.dim() == 2 and t.dtype == torch.float32 and t.is_contiguous() and t.device == dev and t.shape == cos.shape,
+              f"{where}: cos and sin must be contiguous fp32 tables of positions x rot_dim/2")
+    _need(positions.shape == (tokens,) and positions.dtype == torch.int32 and positions.is_contiguous() and positions.device == dev,
+          f"{where}: positions must be {tokens} contiguous int32")
+    wd = DTYPE_F32
+    for w in (q_weight, k_weight):
+        if w is None:
+            continue
+        _need(w.shape == (dim,) and w.is_contiguous() and w.device == dev, f"{where}: a weight must be {dim} contiguous values")
+        wd = _code(w.dtype)
+    _need(q_weight is None or k_weight is None or q_weight.dtype == k_weight.dtype, f"{where}: the weights differ in dtype")
+    _need(k is None or k.shape[0] == tokens, f"{where}: q and k differ in tokens")
+    _need(k is not None or k_weight is None, f"{where}: k_weight without k")
+    return MxRope(tokens, dim, rot, int(interleaved), wd, _raw(q_weight), _raw(k_weight), cos.data_ptr(), sin.data_ptr(),
+                  cos.shape[0], positions.data_ptr(), eps)
+
+
+def _ref(h):
+    return None if h is None else ctypes.byref(h)
+
+
+def mx_qk_rope(q, k, cos, sin, positions, q_weight=None, k_weight=None, eps=1e-6, interleaved=False, q_out=None,
+               k_out=None, stream=None):
+    """RMS norm (where a weight is given) and rotation of query and key heads
+    in one pass.  q, k: tokens x heads x dim, bf16 or fp32, any token and head
+    strides (views of a fused projection); k may be None.  cos, sin: fp32
+    tables of positions x rot_dim/2; positions: int32 per token.  interleaved:
+    pairs (2i, 2i+1) instead of (i, i + rot_dim/2).  q_out, k_out: tensors to
+    write into (q and k themselves included), else new ones.
+    Returns (q_out, k_out)."""
+    _need(q.dim() == 3, "mx_qk_rope: q must be tokens x heads x dim")
+    dev, dim = q.device, q.shape[2]
+    r = _rope_args(q, k, cos, sin, positions, q_weight, k_weight, eps, interleaved, "mx_qk_rope")
+    if q_out is None:
+        q_out = torch.empty(q.shape, dtype=q.dtype, device=dev)
+    hq, ho = _heads(q, dim, dev, "q"), _heads(q_out, dim, dev, "q_out")
+    _need(q_out.shape[0] == q.shape[0], "mx_qk_rope: q_out must have q's shape")
+    hk = hp = None
+    if k is not None:
+        if k_out is None:
+            k_out = torch.empty(k.shape, dtype=k.dtype, device=dev)
+        hk, hp = _heads(k, dim, dev, "k"), _heads(k_out, dim, dev, "k_out")
+        _need(k_out.shape[0] == k.shape[0], "mx_qk_rope: k_out must have k's shape")
+    _check(lib().mx_qk_rope(ctypes.byref(r), ctypes.byref(hq), _ref(hk), ctypes.byref(ho), _ref(hp), _stream_ptr(stream)),
+           "mx_qk_rope")
+    return q_out, k_out
+
+
+def mx_qk_rope_backward(dy_q, dy_k, q, k, cos, sin, positions, q_weight=None, k_weight=None, eps=1e-6,
+                        interleaved=False, dq=None, dk=None, workspace=None, stream=None):
+    """Gradient of mx_qk_rope: dy_q, dy_k are the gradients of its outputs, the
+    rest are its arguments.  Returns (dq, dk, dq_weight, dk_weight); the weight
+    gradients are fp32 (None without that weight).  dq, dk may be dy_q, dy_k."""
+    _need(q.dim() == 3, "mx_qk_rope_backward: q must be tokens x heads x dim")
+    dev, dim = q.device, q.shape[2]
+    r = _rope_args(q, k, cos, sin, positions, q_weight, k_weight, eps, interleaved, "mx_qk_rope_backward")
+    _need((k is None) == (dy_k is None), "mx_qk_rope_backward: dy_k and k go together")
+    sets = []
+    for y, x, d in ((dy_q, q, dq), (dy_k, k, dk)):
+        if x is None:
+            sets.append((None, None, None, None))
+            continue
+        if d is None:
+            d = torch.empty(x.shape, dtype=x.dtype, device=dev)
+        _need(y.shape == x.shape and d.shape == x.shape, "mx_qk_rope_backward: gradients must have their heads' shape")
+        sets.append((d, _heads(y, dim, dev, "dy"), _heads(x, dim, dev, "x"), _heads(d, dim, dev, "dx")))
+    dws = [None if w is None else torch.empty(dim, dtype=torch.float32, device=dev) for w in (q_weight, k_weight)]
+    need = lib().mx_qk_rope_workspace_size(ctypes.byref(r))
+    if workspace is None and need:
+        workspace = _empty(need, dev)
+    (dq, gq, xq, oq), (dk, gk, xk, ok) = sets
+    rc = lib().mx_qk_rope_backward(ctypes.byref(r), ctypes.byref(gq), _ref(gk), ctypes.byref(xq), _ref(xk), ctypes.byref(oq),
+                                   _ref(ok), _raw(dws[0]), _raw(dws[1]), _raw(workspace),
+                                   0 if workspace is None else workspace.numel(), _stream_ptr(stream))
+    _check(rc, "mx_qk_rope_backward")
+    return dq, dk, dws[0], dws[1]
+
+
+@dataclass
+class KVCache:
+    """A paged cache of keys and values.  fmt None: k and v are bf16, pages x
+    heads x page_size x dim.  fmt MXFP8_E4M3 or MXFP4: uint8 codes, pages x
+    heads x page_size x (dim or dim/2), with uint8 E8M0 scales pages x heads x
+    page_size x dim/32."""
+    fmt: Format
+    k: torch.Tensor
+    v: torch.Tensor
+    k_scales: torch.Tensor = None
+    v_scales: torch.Tensor = None
+
+    def __post_init__(self):
+        bits = 16 if self.fmt is None else {ELEM_FP8_E4M3: 8, ELEM_E2M1: 4}.get(self.fmt.elem)
+        _need(bits is not None, "KVCache: the format must have E4M3 or E2M1 elements")
+        dt = torch.bfloat16 if self.fmt is None else torch.uint8
+        _need(self.k.dim() == 4 and self.v.shape == self.k.shape, "KVCache: k and v must be pages x heads x page_size x dim")
+        self.pages, self.heads, self.page_size, last = self.k.shape
+        self.dim = last * 2 if bits == 4 else last
+        need = [(self.k, self.k.shape, dt), (self.v, self.k.shape, dt)]
+        if self.fmt is not None:
+            grid = (*self.k.shape[:3], self.dim // 32)
+            need += [(self.k_scales, grid, torch.uint8), (self.v_scales, grid, torch.uint8)]
+        for t, shape, dtype in need:
+            _need(t is not None and t.shape == shape and t.dtype == dtype and t.is_contiguous() and t.device == self.k.device,
+                  f"KVCache: expected a contiguous {dtype} buffer of {tuple(shape)}")
+
+    def c(self):
+        f = None if self.fmt is None else ctypes.pointer(self.fmt.c())
+        return MxKVCache(f, self.k.data_ptr(), self.v.data_ptr(), _raw(self.k_scales), _raw(self.v_scales), self.pages,
+                         self.page_size, self.heads, self.dim)
+
+
+def alloc_kv_cache(fmt, pages, page_size, heads, dim, device="cuda"):
+    """A KVCache of zeros: fmt None (bf16), MXFP8_E4M3 or MXFP4."""
+    z = lambda last, dtype: torch.zeros((pages, heads, page_size, last), dtype=dtype, device=device)
+    if fmt is None:
+        return KVCache(None, z(dim, torch.bfloat16), z(dim, torch.bfloat16))
+    last = dim // 2 if fmt.elem == ELEM_E2M1 else dim
+    return KVCache(fmt, z(last, torch.uint8), z(last, torch.uint8), z(dim // 32, torch.uint8), z(dim // 32, torch.uint8))
+
+
+def mx_cache_write(cache: KVCache, k, v, slots, stream=None):
+    """Write the keys and values of new tokens (tokens x heads x dim, bf16 or
+    fp32, any token and head strides) to the cache, quantized to its format.
+    slots: int64 per token, page * page_size + position in the page; a slot
+    outside the cache skips its token.  Returns the cache."""
+    dev = cache.k.device
+    hk, hv = _heads(k, cache.dim, dev, "k"), _heads(v, cache.dim, dev, "v")
+    tokens = k.shape[0]
+    _need(v.shape[0] == tokens, "mx_cache_write: k and v differ in tokens")
+    _need(slots.shape == (tokens,) and slots.dtype == torch.int64 and slots.is_contiguous() and slots.device == dev,
+          f"mx_cache_write: slots must be {tokens} contiguous int64")
+    rc = lib().mx_cache_write(ctypes.byref(cache.c()), ctypes.byref(hk), ctypes.byref(hv), tokens, slots.data_ptr(),
+                              _stream_ptr(stream))
+    _check(rc, "mx_cache_write")
+    return cache
+
+
+def mx_attend_workspace_size(cache: KVCache, batch, q_heads, table_cols):
+    return int(lib().mx_attend_workspace_size(ctypes.byref(cache.c()), batch, q_heads, table_cols))
+
+
+def alloc_attend_workspace(cache: KVCache, batch, q_heads, table_cols):
+    return _empty(mx_attend_workspace_size(cache, batch, q_heads, table_cols), cache.k.device)
+
+
+def mx_attend(q, cache: KVCache, page_table, lengths, scale=None, out=None, lse=None, workspace=None, stream=None):
+    """Attention of one new token per sequence over the paged cache.  q: batch x
+    heads x dim (bf16 or fp32; heads a multiple of the cache's); page_table:
+    int32, batch x columns (rows may be strided); lengths: int32 per sequence,
+    0 allowed (out 0, lse -inf).  scale: default dim^-1/2.  lse: None, True
+    (allocate) or a batch x heads fp32 tensor.  workspace: as
+    alloc_attend_workspace gives (allocated when None).
+    Returns out, or (out, lse) when lse is asked for."""
+    _need(q.dim() == 3, "mx_attend: q must be batch x heads x dim")
+    dev = cache.k.device
+    batch, heads, dim = q.shape
+    hq = _heads(q, cache.dim, dev, "q")
+    _need(page_table.dim() == 2 and page_table.shape[0] == batch and page_table.dtype == torch.int32 and
+          page_table.device == dev and (page_table.numel() == 0 or page_table.stride(1) == 1),
+          f"mx_attend: page_table must be {batch} rows of contiguous int32")
+    _need(lengths.shape == (batch,) and lengths.dtype == torch.int32 and lengths.is_contiguous() and lengths.device == dev,
+          f"mx_attend: lengths must be {batch} contiguous int32")
+    if out is None:
+        out = torch.empty((batch, heads, dim), dtype=q.dtype, device=dev)
+    ho = _heads(out, cache.dim, dev, "out")
+    _need(out.shape[0] == batch, "mx_attend: out must have q's shape")
+    if lse is True:
+        lse = torch.empty((batch, heads), dtype=torch.float32, device=dev)
+    elif lse is not None:
+        _need(lse.shape == (batch, heads) and lse.dtype == torch.float32 and lse.is_contiguous() and lse.device == dev,
+              f"mx_attend: lse must be a contiguous fp32 {batch} x {heads}")
+    c = cache.c()
+    cols = page_table.shape[1]
+    if workspace is None:
+        workspace = _empty(lib().mx_attend_workspace_size(ctypes.byref(c), batch, heads, cols), dev)
+    rc = lib().mx_attend(ctypes.byref(c), ctypes.byref(hq), batch, page_table.data_ptr(), cols,
+                         cols if batch <= 1 else page_table.stride(0), lengths.data_ptr(),
+                         dim ** -0.5 if scale is None else scale, ctypes.byref(ho), _raw(lse), workspace.data_ptr(),
+                         workspace.numel(), _stream_ptr(stream))
+    _check(rc, "mx_attend")
+    return out if lse is None else (out, lse)

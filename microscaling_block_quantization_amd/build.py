@@ -19,7 +19,8 @@ LIB = os.path.join(HERE, "libmx.so")
 CEIL_LIB = os.path.join(HERE, "libmx_ceilings.so")
 CEIL_SOURCES = ["ceilings.hip"]
 BUILD = os.path.join(HERE, "_build")
-SOURCES = ["api.hip", "quant_rows.hip", "quant_tiles.hip", "misc.hip", "gemm_mxfp4.hip", "gemm_lds.hip", "gemm_upcvt.hip"]
+SOURCES = ["api.hip", "quant_rows.hip", "quant_tiles.hip", "misc.hip", "gemm_mxfp4.hip", "gemm_lds.hip", "gemm_upcvt.hip",
+           "matvec.hip", "qk_rope.hip", "attend.hip"]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 FLAGS = ["--offload-arch=gfx950", "-O3", "-std=c++17", "-fPIC",

@@ -250,6 +250,101 @@ int static_scratch(uint8_t** ptr) {
     return MX_OK;
 }
 
+// ---- checks of the decode-step entry points --------------------------------
+bool dtype_ok(int d) { return d == MX_DTYPE_F32 || d == MX_DTYPE_BF16; }
+int64_t elem_size(int d) { return d == MX_DTYPE_BF16 ? 2 : 4; }
+
+// A set of heads that a launch over `tokens` tokens reads or writes.
+int check_heads(const mx_heads* h, int64_t tokens) {
+    if (!h || h->heads < 1 || !dtype_ok(h->dtype) || !h->x) return MX_ERR_ARG;
+    const int64_t e = elem_size(h->dtype);
+    if (!aligned16(h->x) || (tokens > 1 && ((h->token_stride * e) & 15)) || (h->heads > 1 && ((h->head_stride * e) & 15)))
+        return MX_ERR_ALIGN;
+    return MX_OK;
+}
+bool same_heads(const mx_heads* a, const mx_heads* b) { return a->heads == b->heads && a->dtype == b->dtype; }
+
+// What both directions of the norm and rotation ask of their description.
+int check_rope(const mx_rope* r) {
+    if (!r || r->tokens < 0) return MX_ERR_ARG;
+    if (r->dim < 8 || r->dim > 1024 || r->dim % 8) return MX_ERR_UNSUPPORTED;
+    if (r->rot_dim < 0 || r->rot_dim > r->dim || r->rot_dim % 2) return MX_ERR_ARG;
+    if (r->interleaved != 0 && r->interleaved != 1) return MX_ERR_ARG;
+    if ((r->q_weight || r->k_weight) && (!dtype_ok(r->w_dtype) || !(r->eps >= 0.0f))) return MX_ERR_ARG;
+    if (r->rot_dim && r->tokens && (!r->cos || !r->sin || !r->positions || r->table_rows < 1)) return MX_ERR_ARG;
+    if (!aligned16(r->q_weight) || !aligned16(r->k_weight) || !aligned16(r->cos) || !aligned16(r->sin) ||
+        !aligned16(r->positions))
+        return MX_ERR_ALIGN;
+    return MX_OK;
+}
+
+mxk::RopeParams rope_params(const mx_rope* r) {
+    mxk::RopeParams p;
+    memset(&p, 0, sizeof(p));
+    p.tokens = r->tokens;
+    p.table_rows = r->table_rows;
+    p.dim = r->dim;
+    p.rot = r->rot_dim;
+    p.adjacent = r->interleaved;
+    p.w_bf16 = r->w_dtype == MX_DTYPE_BF16;
+    p.cos = r->cos;
+    p.sin = r->sin;
+    p.positions = r->positions;
+    p.eps = r->eps;
+    p.set[0].w = r->q_weight;
+    p.set[1].w = r->k_weight;
+    return p;
+}
+
+// A cache; `used`: whether its buffers are going to be touched.
+int check_cache(const mx_kv_cache* c, bool used) {
+    if (!c || c->pages < 0 || c->page_size < 1 || c->page_size > 65536 || c->heads < 1) return MX_ERR_ARG;
+    if (!mxk::attend_dim_ok(c->dim)) return MX_ERR_UNSUPPORTED;
+    if (c->pages > ((int64_t)1 << 40) / c->page_size) return MX_ERR_ARG;
+    if (c->format) {
+        const mx_format* f = c->format;
+        const int rc = check_format(f, 1, c->dim);
+        if (rc) return rc;
+        if ((f->elem != MX_ELEM_FP8_E4M3 && f->elem != MX_ELEM_E2M1) || f->scale != MX_SCALE_E8M0 || f->round != MX_ROUND_RTNE ||
+            f->block_rows != 1 || f->block_cols != 32 || f->asymmetric || f->hadamard || f->macro_cols)
+            return MX_ERR_UNSUPPORTED;
+    }
+    if (!used) return MX_OK;
+    if (c->pages < 1 || !c->k || !c->v || (c->format && (!c->k_scales || !c->v_scales))) return MX_ERR_ARG;
+    if (!aligned16(c->k) || !aligned16(c->v) || !aligned16(c->k_scales) || !aligned16(c->v_scales)) return MX_ERR_ALIGN;
+    return MX_OK;
+}
+
+mxk::KvCache cache_params(const mx_kv_cache* c) {
+    mxk::KvCache k;
+    k.k = static_cast<uint8_t*>(c->k);
+    k.v = static_cast<uint8_t*>(c->v);
+    k.ks = c->format ? static_cast<uint8_t*>(c->k_scales) : nullptr;
+    k.vs = c->format ? static_cast<uint8_t*>(c->v_scales) : nullptr;
+    k.pages = c->pages;
+    k.page = c->page_size;
+    k.heads = c->heads;
+    k.dim = c->dim;
+    k.kind = !c->format ? mxk::KV_BF16 : c->format->elem == MX_ELEM_FP8_E4M3 ? mxk::KV_FP8 : mxk::KV_FP4;
+    return k;
+}
+
+// The shape of an attention call.
+int check_attend(const mx_kv_cache* c, int64_t batch, int32_t q_heads, int64_t cols) {
+    if (batch < 0 || cols < 0 || q_heads < 1 || q_heads % c->heads) return MX_ERR_ARG;
+    if (cols >= ((int64_t)1 << 30) / c->page_size || batch >= (int64_t)1 << 31) return MX_ERR_ARG;
+    int chunk, splits;
+    mxk::attend_plan(cache_params(c), batch, q_heads, cols, &chunk, &splits);
+    if ((double)batch * q_heads * splits >= 2147483648.0) return MX_ERR_ARG;
+    return MX_OK;
+}
+
+size_t attend_bytes(const mx_kv_cache* c, int64_t batch, int32_t q_heads, int64_t cols) {
+    int chunk, splits;
+    mxk::attend_plan(cache_params(c), batch, q_heads, cols, &chunk, &splits);
+    return splits > 1 ? round_up((size_t)batch * q_heads * splits * (c->dim + 2) * sizeof(float)) : 0;
+}
+
 }  // namespace
 
 extern "C" {
@@ -508,6 +603,203 @@ int mx_gemm(const mx_format* fa, const mx_qtensor* a, const mx_format* fb, const
     return hip_status(mxk::launch_gemm(fa->elem, ac, as, fb->elem, bc, bs, c, M, N, K, ldc, cb, s,
                                        fa->macro_cols ? static_cast<const uint8_t*>(a->macro_scales) : nullptr,
                                        fb->macro_cols ? static_cast<const uint8_t*>(b->macro_scales) : nullptr));
+}
+
+int mx_matvec(const mx_format* fw, const mx_qtensor* w, int x_dtype, const void* x, int64_t tokens, int64_t ldx,
+              const void* bias, void* y, int64_t ldy, int y_dtype, void* stream) {
+    if (!fw || !w) return MX_ERR_ARG;
+    int rc = check_format(fw, w->rows, w->cols);
+    if (rc) return rc;
+    if ((fw->elem != MX_ELEM_E2M1 && fw->elem != MX_ELEM_INT4) || fw->scale == MX_SCALE_E3M0 || fw->block_rows != 1 ||
+        fw->hadamard)
+        return MX_ERR_UNSUPPORTED;
+    if (!dtype_ok(x_dtype) || !dtype_ok(y_dtype) || tokens < 0) return MX_ERR_ARG;
+    const int64_t N = w->rows, K = w->cols;
+    if (ldx < K || ldy < N || N >= (int64_t)1 << 31 || K >= (int64_t)1 << 27 || tokens > (int64_t)16 * 65535) return MX_ERR_ARG;
+    if (N == 0 || tokens == 0) return MX_OK;
+    if (K == 0) return MX_ERR_UNSUPPORTED;
+    if (!x || !y || !w->codes || !w->scales) return MX_ERR_ARG;
+    if ((fw->asymmetric && !w->offsets) || (fw->macro_cols && !w->macro_scales) ||
+        (fw->scale == MX_SCALE_NVFP4 && !w->tensor_scale))
+        return MX_ERR_ARG;
+    if (!aligned16(x) || !aligned16(y) || !aligned16(bias) || !aligned16(w->codes) || !aligned16(w->scales) ||
+        ((ldx * elem_size(x_dtype)) & 15))
+        return MX_ERR_ALIGN;
+    if ((fw->asymmetric && !aligned16(w->offsets)) || (fw->macro_cols && !aligned16(w->macro_scales))) return MX_ERR_ALIGN;
+    mxk::MatvecParams p;
+    memset(&p, 0, sizeof(p));
+    p.codes = static_cast<const uint8_t*>(w->codes);
+    p.scales = static_cast<const uint8_t*>(w->scales);
+    p.offsets = fw->asymmetric ? static_cast<const uint16_t*>(w->offsets) : nullptr;
+    p.macro = fw->macro_cols ? static_cast<const uint8_t*>(w->macro_scales) : nullptr;
+    p.tensor_scale = fw->scale == MX_SCALE_NVFP4 ? w->tensor_scale : nullptr;
+    p.n = N;
+    p.k = K;
+    p.elem = fw->elem;
+    p.scale = fw->scale;
+    p.bc = fw->block_cols;
+    p.x = x;
+    p.tokens = tokens;
+    p.ldx = ldx;
+    p.x_bf16 = x_dtype == MX_DTYPE_BF16;
+    p.bias = bias;
+    p.y = y;
+    p.ldy = ldy;
+    p.y_bf16 = y_dtype == MX_DTYPE_BF16;
+    return hip_status(mxk::launch_matvec(p, static_cast<hipStream_t>(stream)));
+}
+
+int mx_qk_rope(const mx_rope* r, const mx_heads* q, const mx_heads* k, const mx_heads* q_out, const mx_heads* k_out,
+               void* stream) {
+    int rc = check_rope(r);
+    if (rc) return rc;
+    if (!q || !q_out || (!k != !k_out)) return MX_ERR_ARG;
+    if (r->tokens == 0) return MX_OK;
+    mxk::RopeParams p = rope_params(r);
+    const mx_heads *in[2] = {q, k}, *out[2] = {q_out, k_out};
+    int64_t heads = 0;
+    for (int i = 0; i < (k ? 2 : 1); i++) {
+        for (const mx_heads* h : {in[i], out[i]}) {
+            rc = check_heads(h, r->tokens);
+            if (rc) return rc;
+            if (h->dtype != q->dtype) return MX_ERR_ARG;
+        }
+        if (!same_heads(in[i], out[i])) return MX_ERR_ARG;
+        mxk::RopeSet& S = p.set[i];
+        S.x = in[i]->x;
+        S.x_ts = in[i]->token_stride;
+        S.x_hs = in[i]->head_stride;
+        S.y = out[i]->x;
+        S.y_ts = out[i]->token_stride;
+        S.y_hs = out[i]->head_stride;
+        S.heads = (uint32_t)in[i]->heads;
+        heads += in[i]->heads;
+    }
+    if (!k) p.set[1].w = nullptr;
+    if (r->tokens >= ((int64_t)1 << 31) / heads) return MX_ERR_ARG;
+    return hip_status(mxk::launch_rope(p, q->dtype == MX_DTYPE_BF16, false, static_cast<hipStream_t>(stream)));
+}
+
+size_t mx_qk_rope_workspace_size(const mx_rope* r) {
+    if (check_rope(r) || (!r->q_weight && !r->k_weight)) return 0;
+    return round_up((size_t)2 * mxk::ROPE_PARTS * r->dim * sizeof(float));
+}
+
+int mx_qk_rope_backward(const mx_rope* r, const mx_heads* dy_q, const mx_heads* dy_k, const mx_heads* q,
+                        const mx_heads* k, const mx_heads* dq, const mx_heads* dk, float* dq_weight, float* dk_weight,
+                        void* workspace, size_t ws_bytes, void* stream) {
+    int rc = check_rope(r);
+    if (rc) return rc;
+    if (!q || !dy_q || !dq || (!k != !dy_k) || (!k != !dk)) return MX_ERR_ARG;
+    mxk::RopeParams p = rope_params(r);
+    if (!k) p.set[1].w = nullptr;
+    if (!p.set[0].w != !dq_weight || !p.set[1].w != !dk_weight) return MX_ERR_ARG;
+    const mx_heads *gy[2] = {dy_q, dy_k}, *in[2] = {q, k}, *out[2] = {dq, dk};
+    int64_t heads = 0;
+    for (int i = 0; i < (k ? 2 : 1) && r->tokens; i++) {
+        for (const mx_heads* h : {gy[i], in[i], out[i]}) {
+            rc = check_heads(h, r->tokens);
+            if (rc) return rc;
+            if (h->dtype != q->dtype || h->heads != in[i]->heads) return MX_ERR_ARG;
+        }
+        mxk::RopeSet& S = p.set[i];
+        S.x = in[i]->x;
+        S.x_ts = in[i]->token_stride;
+        S.x_hs = in[i]->head_stride;
+        S.g = gy[i]->x;
+        S.g_ts = gy[i]->token_stride;
+        S.g_hs = gy[i]->head_stride;
+        S.y = out[i]->x;
+        S.y_ts = out[i]->token_stride;
+        S.y_hs = out[i]->head_stride;
+        S.heads = (uint32_t)in[i]->heads;
+        heads += in[i]->heads;
+    }
+    if (heads && r->tokens >= ((int64_t)1 << 31) / heads) return MX_ERR_ARG;
+    if (!aligned16(dq_weight) || !aligned16(dk_weight)) return MX_ERR_ALIGN;
+    if (p.set[0].w || p.set[1].w) {
+        if (!workspace || ws_bytes < mx_qk_rope_workspace_size(r)) return MX_ERR_WORKSPACE;
+        if (!aligned16(workspace)) return MX_ERR_ALIGN;
+    }
+    p.set[0].dw = dq_weight;
+    p.set[1].dw = dk_weight;
+    p.set[0].parts = static_cast<float*>(workspace);
+    return hip_status(mxk::launch_rope(p, q->dtype == MX_DTYPE_BF16, true, static_cast<hipStream_t>(stream)));
+}
+
+int mx_cache_write(const mx_kv_cache* cache, const mx_heads* k, const mx_heads* v, int64_t tokens, const int64_t* slots,
+                   void* stream) {
+    if (tokens < 0) return MX_ERR_ARG;
+    int rc = check_cache(cache, tokens > 0);
+    if (rc) return rc;
+    if (tokens == 0) return MX_OK;
+    for (const mx_heads* h : {k, v}) {
+        rc = check_heads(h, tokens);
+        if (rc) return rc;
+        if (h->heads != cache->heads || h->dtype != k->dtype) return MX_ERR_ARG;
+    }
+    if (!slots || tokens >= ((int64_t)1 << 30) / cache->heads) return MX_ERR_ARG;
+    if (!aligned16(slots)) return MX_ERR_ALIGN;
+    mxk::CacheWrite p;
+    memset(&p, 0, sizeof(p));
+    p.c = cache_params(cache);
+    p.k = k->x;
+    p.v = v->x;
+    p.k_ts = k->token_stride;
+    p.k_hs = k->head_stride;
+    p.v_ts = v->token_stride;
+    p.v_hs = v->head_stride;
+    p.slots = slots;
+    p.tokens = tokens;
+    p.rule = cache->format ? cache->format->rule : 0;
+    p.tau = cache->format ? cache->format->oas_tau : 0.0f;
+    return hip_status(mxk::launch_cache_write(p, k->dtype == MX_DTYPE_BF16, static_cast<hipStream_t>(stream)));
+}
+
+size_t mx_attend_workspace_size(const mx_kv_cache* cache, int64_t batch, int32_t q_heads, int64_t table_cols) {
+    if (check_cache(cache, false) || check_attend(cache, batch, q_heads, table_cols)) return 0;
+    return attend_bytes(cache, batch, q_heads, table_cols);
+}
+
+int mx_attend(const mx_kv_cache* cache, const mx_heads* q, int64_t batch, const int32_t* page_table, int64_t table_cols,
+              int64_t table_stride, const int32_t* lengths, float scale, const mx_heads* out, float* lse,
+              void* workspace, size_t ws_bytes, void* stream) {
+    if (batch < 0 || table_cols < 0) return MX_ERR_ARG;
+    int rc = check_cache(cache, batch > 0 && table_cols > 0);
+    if (rc) return rc;
+    if (batch == 0) return MX_OK;
+    for (const mx_heads* h : {q, out}) {
+        rc = check_heads(h, batch);
+        if (rc) return rc;
+    }
+    if (!same_heads(q, out)) return MX_ERR_ARG;
+    rc = check_attend(cache, batch, q->heads, table_cols);
+    if (rc) return rc;
+    if (!lengths || (table_cols && !page_table) || (batch > 1 && table_stride < table_cols)) return MX_ERR_ARG;
+    if (!aligned16(lse)) return MX_ERR_ALIGN;
+    const size_t need = attend_bytes(cache, batch, q->heads, table_cols);
+    if (need && (!workspace || ws_bytes < need)) return MX_ERR_WORKSPACE;
+    if (need && !aligned16(workspace)) return MX_ERR_ALIGN;
+    mxk::AttendParams p;
+    memset(&p, 0, sizeof(p));
+    p.c = cache_params(cache);
+    p.q = q->x;
+    p.q_ts = q->token_stride;
+    p.q_hs = q->head_stride;
+    p.o = out->x;
+    p.o_ts = out->token_stride;
+    p.o_hs = out->head_stride;
+    p.batch = batch;
+    p.q_heads = q->heads;
+    p.table = page_table;
+    p.cols = table_cols;
+    p.table_stride = table_stride;
+    p.lengths = lengths;
+    p.scale = scale;
+    p.lse = lse;
+    p.parts = static_cast<float*>(workspace);
+    mxk::attend_plan(p.c, batch, q->heads, table_cols, &p.chunk, &p.splits);
+    return hip_status(mxk::launch_attend(p, q->dtype == MX_DTYPE_BF16, static_cast<hipStream_t>(stream)));
 }
 
 }  // extern "C"

@@ -1,0 +1,278 @@
+"""The paged key-value cache: writes against the CPU oracle's quantizer, bit
+for bit, and the attention of one new token against float64.
+
+Tolerances of the attention, u = 2^-23.  A score z = scale q.k is off by at
+most dz = (D + 16) u |scale| sum |q k|, so a probability by a factor of
+1 + 2 dz (plus 8 u for the exponential and its argument's scaling, times 1 +
+|z|).  Probabilities enter the sum over values as two bf16 parts (off by
+2^-16) or, for fp32 queries, three (2^-23), and n terms are summed in fp32.
+So an output is off by at most (4 max dz + 16 u (1 + max |z|) + 2^-16 or u +
+2 (n + 64) u) sum p |v|, and lse by max dz + (n + 64) u + 16 u (1 + max |z| +
+|lse|).  A bf16 output adds 2^-8 of its magnitude."""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+import microscaling_block_quantization_amd as mx
+import oracle
+
+pytestmark = pytest.mark.gpu
+U = 2.0 ** -23
+FORMATS = {"bf16": None, "mxfp8": mx.MXFP8_E4M3, "mxfp4": mx.MXFP4}
+
+
+def bits(t):
+    return t.contiguous().view(torch.int16).cpu().numpy().view(np.uint16)
+
+
+# ---- writes ---------------------------------------------------------------------
+@pytest.mark.parametrize("kind", ["bf16", "mxfp8", "mxfp4", "mxfp8 ceil", "mxfp4 oas"])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("dim,heads,page", [(128, 8, 16), (64, 1, 7), (96, 3, 64), (256, 2, 1)])
+def test_write(kind, dtype, dim, heads, page):
+    fmt = {"mxfp8 ceil": mx.Format(elem=mx.ELEM_FP8_E4M3, rule=mx.RULE_CEIL),
+           "mxfp4 oas": mx.Format(rule=mx.RULE_OAS, oas_tau=7.5)}.get(kind, FORMATS.get(kind))
+    rng = np.random.default_rng(dim + page)
+    t = 37
+    x = rng.standard_normal((t, 2 * heads + 1, dim)).astype(np.float32) * np.exp(rng.uniform(-30, 30, (t, 1, 1))).astype(np.float32)
+    x[3, 0] = 0
+    x[4, heads, 5] = np.inf
+    x[5, 1, 33] = np.nan
+    x[6, 0, :32] = 3e38
+    x[7, 0, 32:64] = 1e-40
+    x = torch.from_numpy(x).cuda().to(dtype)
+    k, v = x[:, :heads], x[:, heads + 1:]                 # strided, as a fused projection leaves them
+    pages = -(-t // page) + 3
+    cache = mx.alloc_kv_cache(fmt, pages, page, heads, dim)
+    for b in (cache.k, cache.v):
+        b.fill_(9)
+    slots = torch.from_numpy(rng.permutation(pages * page)[:t].astype(np.int64)).cuda()
+    slots[10], slots[11] = -1, pages * page               # skipped
+    before = cache.k.clone()
+    mx.mx_cache_write(cache, k, v, slots)
+    torch.cuda.synchronize()
+    at = slots.cpu().numpy()
+    written = np.zeros(pages * page, bool)
+    for i in range(t):
+        if 0 <= at[i] < pages * page:
+            written[at[i]] = True
+    for src, dst, sc in ((k, cache.k, cache.k_scales), (v, cache.v, cache.v_scales)):
+        got = dst.permute(0, 2, 1, 3).reshape(pages * page, heads, -1)
+        assert torch.equal(got[torch.from_numpy(~written).cuda()].float(),
+                           before.permute(0, 2, 1, 3).reshape(pages * page, heads, -1)[torch.from_numpy(~written).cuda()].float())
+        rows = [i for i in range(t) if 0 <= at[i] < pages * page]
+        got = got[slots[rows]]
+        want = src[rows]
+        if fmt is None:
+            w = oracle.f32_to_bf16_bits(want.float().contiguous().cpu().numpy())
+            assert np.array_equal(bits(got), w)
+            continue
+        host = want.contiguous().float().cpu().numpy() if dtype == torch.float32 else bits(want)
+        r = oracle.quantize(host.reshape(-1, dim), oracle.Format(elem=fmt.elem, rule=fmt.rule, oas_tau=fmt.oas_tau))
+        assert np.array_equal(got.cpu().numpy().reshape(r["codes"].shape), r["codes"])
+        gsc = sc.permute(0, 2, 1, 3).reshape(pages * page, heads, -1)[slots[rows]]
+        assert np.array_equal(gsc.cpu().numpy().reshape(r["scales"].shape), r["scales"])
+    assert mx.mx_cache_write(cache, k[:0], v[:0], slots[:0]) is cache
+
+
+# ---- attention -------------------------------------------------------------------
+def values64(cache, what):
+    """Every cached value in float64: pages x heads x page x dim"""
+    t = cache.k if what == "k" else cache.v
+    if cache.fmt is None:
+        return t.double().cpu().numpy()
+    sc = cache.k_scales if what == "k" else cache.v_scales
+    codes = t.cpu().numpy()
+    p, h, n, last = codes.shape
+    rows = p * h * n
+    f = oracle.Format(elem=cache.fmt.elem)
+    y = oracle.dequantize(f, {"codes": codes.reshape(rows, last), "scales": sc.cpu().numpy().reshape(rows, -1)}, rows, cache.dim)
+    return y.astype(np.float64).reshape(p, h, n, cache.dim)
+
+
+def poisoned_cache(kind, pages, page, heads, dim):
+    """A cache in which everything that is not written reads as NaN."""
+    cache = mx.alloc_kv_cache(FORMATS[kind], pages, page, heads, dim)
+    if cache.fmt is None:
+        cache.k.fill_(float("nan"))
+        cache.v.fill_(float("inf"))
+    else:
+        cache.k.fill_(0x7F)
+        cache.v.fill_(0x7F)
+        cache.k_scales.fill_(0xFF)
+        cache.v_scales.fill_(0xFF)
+    return cache
+
+
+def build(kind, lengths, hk, dim, page, seed=0, extra_cols=1, spread=1.0):
+    """A poisoned cache whose sequences' tokens are written through
+    mx_cache_write, their pages scattered; the table's unused entries point
+    outside the cache."""
+    g = torch.Generator(device="cuda").manual_seed(seed + dim + page)
+    used = [-(-n // page) for n in lengths]
+    cols = max(used + [0]) + extra_cols
+    pages = sum(used) + 2
+    cache = poisoned_cache(kind, pages, page, hk, dim)
+    order = torch.randperm(pages, generator=g, device="cuda").to(torch.int32)
+    table = torch.full((len(lengths), cols + 3), -5, device="cuda", dtype=torch.int32)[:, :cols]
+    at = 0
+    for b, u in enumerate(used):
+        table[b, :u] = order[at:at + u]
+        at += u
+    for b, n in enumerate(lengths):
+        if n == 0:
+            continue
+        t = torch.arange(n, device="cuda")
+        slots = table[b, (t // page)].long() * page + t % page
+        kv = torch.randn(n, 2 * hk, dim, generator=g, device="cuda")
+        kv[:, :hk] *= spread
+        kv = kv.to(torch.bfloat16)
+        mx.mx_cache_write(cache, kv[:, :hk], kv[:, hk:], slots.contiguous())
+    return cache, table, torch.tensor(lengths, device="cuda", dtype=torch.int32)
+
+
+def check_attend(cache, table, lengths, q, scale, out, lse, label=""):
+    k64, v64 = values64(cache, "k"), values64(cache, "v")
+    q64 = q.double().cpu().numpy()
+    tab, n_of = table.cpu().numpy(), lengths.cpu().numpy()
+    o, ls = out.double().cpu().numpy(), lse.double().cpu().numpy()
+    batch, hq, dim = q64.shape
+    per = hq // cache.heads
+    for b in range(batch):
+        n = min(max(int(n_of[b]), 0), tab.shape[1] * cache.page_size)
+        if n == 0:
+            assert (o[b] == 0).all() and (ls[b] == -np.inf).all(), f"{label}: empty row {b}"
+            continue
+        t = np.arange(n)
+        pg, off = tab[b, t // cache.page_size], t % cache.page_size
+        for h in range(hq):
+            K, V = k64[pg, h // per, off], v64[pg, h // per, off]
+            z = scale * (K @ q64[b, h])
+            dz = ((dim + 16) * U * abs(scale) * (np.abs(K) @ np.abs(q64[b, h]))).max()
+            zm = np.abs(z).max()
+            p = np.exp(z - z.max())
+            want = p @ V / p.sum()
+            parts = 2.0 ** -16 if out.dtype == torch.bfloat16 else U
+            tol = (4 * dz + 16 * U * (1 + zm) + parts + 2 * (n + 64) * U) * (p @ np.abs(V) / p.sum())
+            if out.dtype == torch.bfloat16:
+                tol = tol + 2.0 ** -8 * (np.abs(want) + tol)
+            err = np.abs(o[b, h] - want)
+            assert (err <= tol).all(), f"{label} b{b} h{h}: {np.max(err / tol):.2f} of the tolerance"
+            w = z.max() + math.log(p.sum())
+            assert abs(ls[b, h] - w) <= dz + (n + 64) * U + 16 * U * (1 + zm + abs(w)), f"{label} b{b} h{h}: lse"
+
+
+def run(kind, lengths, group, hk, dim, page, dtype, seed=0, scale=None, **kw):
+    print(kind, lengths, group, hk, dim, page, dtype, flush=True)
+    cache, table, n = build(kind, lengths, hk, dim, page, seed, **kw)
+    q = torch.randn(len(lengths), group * hk, dim, device="cuda", generator=torch.Generator(device="cuda").manual_seed(seed)).to(dtype)
+    s = dim ** -0.5 if scale is None else scale
+    ws = mx.alloc_attend_workspace(cache, len(lengths), group * hk, table.shape[1]).fill_(0xFF)
+    out, lse = mx.mx_attend(q, cache, table, n, scale=s, lse=True, workspace=ws)
+    check_attend(cache, table, n, q, s, out, lse, f"{kind} {lengths} {group}x{hk} {dim}")
+    return cache, table, n, q, out, lse
+
+
+@pytest.mark.parametrize("kind", FORMATS)
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("dim", [64, 96, 128, 192, 256])
+def test_lengths_and_dims(kind, dtype, dim):
+    run(kind, [0, 1, 15, 16, 17, 33, 128, 129], 4, 2, dim, 16, dtype)
+    run(kind, [300, 0, 77], 1, 3, dim, 24, dtype)
+
+
+@pytest.mark.parametrize("kind", FORMATS)
+@pytest.mark.parametrize("page", [1, 3, 16, 24, 48, 100, 128])
+def test_page_sizes(kind, page):
+    run(kind, [5, 257, 96], 8, 1, 128, page, torch.bfloat16)
+
+
+@pytest.mark.parametrize("group", [1, 2, 7, 15, 16, 17, 33])
+def test_group_sizes(group):
+    run("bf16", [190, 40], group, 2, 64, 16, torch.bfloat16)
+    run("mxfp8", [190], group, 1, 128, 32, torch.float32)
+
+
+@pytest.mark.parametrize("kind", FORMATS)
+def test_long_splits(kind):
+    """One sequence over many workgroups, and a batch whose short rows leave most of theirs idle."""
+    run(kind, [9001], 4, 2, 128, 16, torch.bfloat16)
+    run(kind, [5000, 1, 0, 130], 2, 1, 64, 64, torch.float32)
+
+
+def test_peaked_scores():
+    """Scores of hundreds: the running maximum grows and old sums vanish."""
+    run("bf16", [777, 200], 4, 2, 128, 16, torch.bfloat16, spread=40.0)
+    run("mxfp8", [777], 4, 2, 64, 16, torch.float32, spread=40.0, scale=-0.7)
+
+
+def test_scale_zero_and_no_columns():
+    run("bf16", [100], 2, 2, 64, 16, torch.bfloat16, scale=0.0)
+    cache = mx.alloc_kv_cache(None, 1, 16, 2, 64)
+    q = torch.randn(3, 4, 64, device="cuda").to(torch.bfloat16)
+    out, lse = mx.mx_attend(q, cache, torch.empty((3, 0), dtype=torch.int32, device="cuda"),
+                            torch.tensor([0, 5, -3], dtype=torch.int32, device="cuda"), lse=True)
+    assert (out == 0).all() and (lse == -math.inf).all()
+    assert mx.mx_attend(q[:0], cache, torch.empty((0, 2), dtype=torch.int32, device="cuda"),
+                        torch.empty(0, dtype=torch.int32, device="cuda")).shape == (0, 4, 64)
+
+
+@pytest.mark.parametrize("page", [16, 10])
+def test_lengths_past_the_table_and_bad_pages(page):
+    cache, table, n, q, out, lse = run("bf16", [64, 40, 90], 2, 2, 64, page, torch.bfloat16, extra_cols=0)
+    cols = table.shape[1]
+    over = n.clone()
+    full = torch.tensor([cols * page], dtype=torch.int32, device="cuda")
+    row = int(n.argmax())
+    cache.k.nan_to_num_(0.5)
+    cache.v.nan_to_num_(0.5, 0.5, 0.5)
+    over[row] = cols * page + 1000                        # counts as the whole table
+    a = mx.mx_attend(q, cache, table.contiguous(), over)
+    over[row] = full[0]
+    assert torch.equal(a[row], mx.mx_attend(q, cache, table.contiguous(), over)[row])
+    bad = table.clone()
+    bad[0, 0], bad[1, 1] = cache.pages, -1
+    got, l2 = mx.mx_attend(q, cache, bad, n, lse=True)
+    assert got[:2].isnan().all() and l2[:2].isnan().all()
+    assert torch.equal(got[2], mx.mx_attend(q, cache, table.contiguous(), n)[2])
+
+
+def test_non_finite_values_in_use():
+    """A NaN key poisons its own sequence and head alone; so does an infinite value."""
+    cache, table, n, q, out, lse = run("bf16", [50, 60], 2, 2, 128, 16, torch.float32)
+    p = int(table[1, 2])
+    cache.k[p, 1, 3, 9] = float("nan")
+    got, l2 = mx.mx_attend(q, cache, table, n, lse=True)
+    assert got[1, 2:].isnan().all() and l2[1, 2:].isnan().all()
+    assert torch.equal(got[0], out[0]) and torch.equal(got[1, :2], out[1, :2])
+
+
+def test_strided_heads_out_and_same_bits():
+    cache, table, n, q, out, lse = run("mxfp4", [3000, 200], 4, 2, 128, 16, torch.bfloat16)
+    wide = torch.zeros(2, 3, 8, 128, device="cuda", dtype=torch.bfloat16)
+    wide[:, 1] = q
+    dst = torch.full((2, 8, 3, 128), 5.0, device="cuda", dtype=torch.bfloat16)
+    for _ in range(3):
+        mx.mx_attend(wide[:, 1], cache, table, n, out=dst[:, :, 1])
+        assert torch.equal(dst[:, :, 1], out)
+    assert (dst[:, :, 0] == 5).all() and (dst[:, :, 2] == 5).all()
+
+
+def test_offsets_past_32_bits():
+    """A cache over 4 GiB per side, its sequence in the last pages."""
+    pages, heads, page, dim = 2200, 4, 2048, 128
+    assert pages * heads * page * dim * 2 > 1 << 32
+    k = torch.empty((pages, heads, page, dim), dtype=torch.bfloat16, device="cuda")
+    cache = mx.KVCache(None, k, torch.empty_like(k))
+    n = 2500
+    table = torch.tensor([[pages - 1, pages - 2]], dtype=torch.int32, device="cuda")
+    t = torch.arange(n, device="cuda")
+    slots = table[0, t // page].long() * page + t % page
+    kv = torch.randn(n, 2 * heads, dim, device="cuda").to(torch.bfloat16)
+    mx.mx_cache_write(cache, kv[:, :heads], kv[:, heads:], slots)
+    q = torch.randn(1, 8, dim, device="cuda").to(torch.bfloat16)
+    out, lse = mx.mx_attend(q, cache, table, torch.tensor([n], dtype=torch.int32, device="cuda"), lse=True)
+    small = mx.KVCache(None, k[-2:].clone(), cache.v[-2:].clone())
+    check_attend(small, torch.tensor([[1, 0]]), torch.tensor([n]), q, dim ** -0.5, out, lse, "far pages")
