@@ -123,12 +123,12 @@ hipError_t launch_gemm_upcvt(int sca, int bca, const uint8_t* a, const uint8_t* 
 // ---- the decode step (matvec.hip, qk_rope.hip, attend.hip) --------------------
 struct MatvecParams {
     const uint8_t* codes;          // n x k/2
-    const uint8_t* scales;         // n x k/bc
-    const uint16_t* offsets;       // nullable: bf16, n x k/bc
+    const uint8_t* scales;         // n x k / block
+    const uint16_t* offsets;       // nullable: bf16, n x k / block
     const uint8_t* macro;          // nullable: UE4M3, n x k/128
     const float* tensor_scale;     // nullable
     int64_t n, k;
-    int elem, scale, bc;
+    int elem, scale, lgb;          // lgb: log2 of the block width
     const void* x;                 // tokens x k, row stride ldx
     int64_t tokens, ldx;
     int x_bf16;
@@ -136,9 +136,8 @@ struct MatvecParams {
     void* y;
     int64_t ldy;
     int y_bf16;
-    int kc;                        // set by the launcher: K values staged at once
 };
-hipError_t launch_matvec(MatvecParams p, hipStream_t s);
+hipError_t launch_matvec(const MatvecParams& p, hipStream_t s);
 
 // queries or keys of a norm-and-rotation launch; strides in elements
 struct RopeSet {
