@@ -18,6 +18,7 @@ blocks (ARITH 2025 MX-training report, main results).
 """
 import ctypes
 import os
+import struct
 from dataclasses import dataclass, field
 
 import torch
@@ -122,17 +123,17 @@ def lib():
         L.mx_qsnr.argtypes = [i32, vp, vp, i64, P(MxStats), P(ctypes.c_double), vp,
                               ctypes.c_size_t, vp]
         L.mx_gemm.argtypes = [P(MxFormat), P(MxQTensor), P(MxFormat), P(MxQTensor), vp, i64, i32, vp]
+        # structs of these calls are passed as packed bytes or by reference
         sz = ctypes.c_size_t
-        L.mx_matvec.argtypes = [P(MxFormat), P(MxQTensor), i32, vp, i64, i64, vp, vp, i64, i32, vp]
-        H = P(MxHeads)
-        L.mx_qk_rope.argtypes = [P(MxRope), H, H, H, H, vp]
-        L.mx_qk_rope_workspace_size.argtypes = [P(MxRope)]
+        L.mx_matvec.argtypes = [vp, vp, i32, vp, i64, i64, vp, vp, i64, i32, vp]
+        L.mx_qk_rope.argtypes = [vp] * 6
+        L.mx_qk_rope_workspace_size.argtypes = [vp]
         L.mx_qk_rope_workspace_size.restype = sz
-        L.mx_qk_rope_backward.argtypes = [P(MxRope), H, H, H, H, H, H, vp, vp, vp, sz, vp]
-        L.mx_cache_write.argtypes = [P(MxKVCache), H, H, i64, vp, vp]
-        L.mx_attend_workspace_size.argtypes = [P(MxKVCache), i64, ctypes.c_int32, i64]
+        L.mx_qk_rope_backward.argtypes = [vp] * 10 + [sz, vp]
+        L.mx_cache_write.argtypes = [vp, vp, vp, i64, vp, vp]
+        L.mx_attend_workspace_size.argtypes = [vp, i64, ctypes.c_int32, i64]
         L.mx_attend_workspace_size.restype = sz
-        L.mx_attend.argtypes = [P(MxKVCache), H, i64, vp, i64, i64, vp, ctypes.c_float, H, vp, vp, sz, vp]
+        L.mx_attend.argtypes = [vp, vp, i64, vp, i64, i64, vp, ctypes.c_float, vp, vp, vp, sz, vp]
         L.mx_status_string.argtypes = [i32]
         L.mx_status_string.restype = ctypes.c_char_p
         for name in ("mx_query_sizes", "mx_quantize", "mx_quantize_noalloc", "mx_quantize_many",
@@ -389,9 +390,14 @@ def mx_gemm(fa: Format, a: QTensor, fb: Format, b: QTensor, c=None, out_dtype=to
 
 
 # ---- one decode step with quantized weights and a quantized cache ------------
-# These calls are small enough that the host's share counts: arguments are
-# packed with as few steps as their checks allow.
+# These kernels take a few microseconds, so the host's share of a call counts:
+# each check is one cheap comparison whose message is only formed when it
+# fails, and structs are packed as bytes.
 _DTYPES = {torch.float32: DTYPE_F32, torch.bfloat16: DTYPE_BF16}
+_PACK_FORMAT = struct.Struct("@9if2Q").pack
+_PACK_QTENSOR = struct.Struct("@6P2q").pack
+_PACK_HEADS = struct.Struct("@Pqqii").pack
+_PACK_ROPE = struct.Struct("@q4i4PqPf4x").pack
 
 
 def _code(dtype):
@@ -402,24 +408,28 @@ def _code(dtype):
 
 
 def _stream_ptr(stream):
-    return torch.cuda.current_stream().cuda_stream if stream is None else stream.cuda_stream
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+    return stream.cuda_stream
 
 
 def _raw(t):
-    return None if t is None else t.data_ptr()
+    return 0 if t is None else t.data_ptr()
 
 
-def _need(cond, what):
-    if not cond:
-        raise ValueError(what)
-
-
-def _heads(t, dim, device, what):
-    """An mx_heads of a tokens x heads x dim tensor whose last dimension is contiguous."""
-    if t.dim() != 3 or t.shape[2] != dim or t.stride(2) != 1 or t.device != device:
-        raise ValueError(f"{what}: expected tokens x heads x {dim} on {device}, the last dimension contiguous")
+def _heads(t, dim, dev, what):
+    """The mx_heads of a tokens x heads x dim tensor whose last dimension is contiguous."""
     st = t.stride()
-    return MxHeads(t.data_ptr(), st[0], st[1], t.shape[1], _code(t.dtype))
+    if len(st) != 3 or t.size(2) != dim or st[2] != 1 or t.get_device() != dev:
+        raise ValueError(f"{what}: expected tokens x heads x {dim} on one device, the last dimension contiguous")
+    return _PACK_HEADS(t.data_ptr(), st[0], st[1], t.size(1), _code(t.dtype))
+
+
+def _vector(t, n, dtype, dev, what):
+    """Checks n contiguous values (of dtype, unless None)."""
+    if t.dim() != 1 or t.size(0) != n or not t.is_contiguous() or t.get_device() != dev or (dtype is not None and t.dtype != dtype):
+        raise ValueError(f"{what}: expected {n} contiguous values{'' if dtype is None else f' of {dtype}'} on the inputs' device")
+    return t.data_ptr()
 
 
 def mx_matvec(fmt: Format, w: QTensor, x: torch.Tensor, bias=None, y=None, out_dtype=None, stream=None):
@@ -427,51 +437,60 @@ def mx_matvec(fmt: Format, w: QTensor, x: torch.Tensor, bias=None, y=None, out_d
     or fp32, any row stride) and a 4-bit weight W (N x K: E2M1 or INT4 in row
     blocks, see include/mx.h).  bias: None or N values of x's dtype.  y: a
     tokens x N view to write into, else a new tensor of out_dtype (default: x's)."""
-    _need(x.dim() == 2 and x.shape[1] == w.cols and x.device == w.codes.device and (x.shape[0] == 0 or x.stride(1) == 1),
-          f"mx_matvec: x must be tokens x {w.cols} with contiguous rows on the weight's device")
-    tokens = x.shape[0]
-    xd = _code(x.dtype)
-    if bias is not None:
-        _need(bias.shape == (w.rows,) and bias.dtype == x.dtype and bias.is_contiguous() and bias.device == x.device,
-              f"mx_matvec: bias must be {w.rows} contiguous values of x's dtype")
+    n, k = w.rows, w.cols
+    if x.dim() != 2 or x.size(1) != k or x.get_device() != w.codes.get_device():
+        raise ValueError(f"mx_matvec: x must be tokens x {k} on the weight's device")
+    tokens, dev = x.size(0), x.get_device()
+    ldx, last = x.stride()
+    if last != 1 and k > 1 and tokens:
+        raise ValueError("mx_matvec: the rows of x must be contiguous")
+    bp = 0 if bias is None else _vector(bias, n, x.dtype, dev, "mx_matvec: bias")
     if y is None:
-        y = torch.empty((tokens, w.rows), dtype=x.dtype if out_dtype is None else out_dtype, device=x.device)
+        y = x.new_empty((tokens, n)) if out_dtype is None else x.new_empty((tokens, n), dtype=out_dtype)
+        ldy = n
     else:
-        _need(y.shape == (tokens, w.rows) and (y.numel() == 0 or y.stride(1) == 1) and y.device == x.device,
-              f"mx_matvec: y must be {tokens} x {w.rows} with contiguous rows")
-    one = tokens <= 1
-    rc = lib().mx_matvec(ctypes.byref(fmt.c()), ctypes.byref(w.c()), xd, x.data_ptr(), tokens,
-                         w.cols if one else x.stride(0), _raw(bias), y.data_ptr(), w.rows if one else y.stride(0),
-                         _code(y.dtype), _stream_ptr(stream))
-    _check(rc, "mx_matvec")
+        if y.dim() != 2 or y.size(0) != tokens or y.size(1) != n or (y.stride(1) != 1 and n > 1 and tokens) or y.get_device() != dev:
+            raise ValueError(f"mx_matvec: y must be {tokens} x {n} with contiguous rows")
+        ldy = y.stride(0)
+    if tokens <= 1:
+        ldx, ldy = k, n
+    f = _PACK_FORMAT(fmt.elem, fmt.scale, fmt.rule, fmt.round, fmt.block_rows, fmt.block_cols, fmt.asymmetric, fmt.hadamard,
+                     fmt.macro_cols, fmt.oas_tau, fmt.seed, fmt.rng_offset)
+    q = _PACK_QTENSOR(w.codes.data_ptr(), w.scales.data_ptr(), _raw(w.offsets), _raw(w.macro_scales), _raw(w.tensor_scale), 0, n, k)
+    _check(lib().mx_matvec(f, q, _code(x.dtype), x.data_ptr(), tokens, ldx, bp, y.data_ptr(), ldy, _code(y.dtype),
+                           _stream_ptr(stream)), "mx_matvec")
     return y
 
 
 def _rope_args(q, k, cos, sin, positions, q_weight, k_weight, eps, interleaved, where):
     """The mx_rope of a call, its shapes checked."""
     tokens, _, dim = q.shape
-    rot = 2 * cos.shape[1]
-    dev = q.device
+    dev = q.get_device()
+    rows, half = cos.shape
     for t in (cos, sin):
-        _need(t.dim() == 2 and t.dtype == torch.float32 and t.is_contiguous() and t.device == dev and t.shape == cos.shape,
-              f"{where}: cos and sin must be contiguous fp32 tables of positions x rot_dim/2")
-    _need(positions.shape == (tokens,) and positions.dtype == torch.int32 and positions.is_contiguous() and positions.device == dev,
-          f"{where}: positions must be {tokens} contiguous int32")
+        if t.dtype != torch.float32 or not t.is_contiguous() or t.get_device() != dev or t.size(0) != rows or t.size(1) != half:
+            raise ValueError(f"{where}: cos and sin must be contiguous fp32 tables of positions x rot_dim/2")
+    pos = _vector(positions, tokens, torch.int32, dev, where + ": positions")
     wd = DTYPE_F32
-    for w in (q_weight, k_weight):
-        if w is None:
-            continue
-        _need(w.shape == (dim,) and w.is_contiguous() and w.device == dev, f"{where}: a weight must be {dim} contiguous values")
-        wd = _code(w.dtype)
-    _need(q_weight is None or k_weight is None or q_weight.dtype == k_weight.dtype, f"{where}: the weights differ in dtype")
-    _need(k is None or k.shape[0] == tokens, f"{where}: q and k differ in tokens")
-    _need(k is not None or k_weight is None, f"{where}: k_weight without k")
-    return MxRope(tokens, dim, rot, int(interleaved), wd, _raw(q_weight), _raw(k_weight), cos.data_ptr(), sin.data_ptr(),
-                  cos.shape[0], positions.data_ptr(), eps)
+    qp = kp = 0
+    if q_weight is not None:
+        qp, wd = _vector(q_weight, dim, None, dev, where + ": q_weight"), _code(q_weight.dtype)
+    if k_weight is not None:
+        if k is None or (q_weight is not None and q_weight.dtype != k_weight.dtype):
+            raise ValueError(f"{where}: k_weight needs k, and the dtype of q_weight")
+        kp, wd = _vector(k_weight, dim, None, dev, where + ": k_weight"), _code(k_weight.dtype)
+    if k is not None and k.size(0) != tokens:
+        raise ValueError(f"{where}: q and k differ in tokens")
+    return _PACK_ROPE(tokens, dim, 2 * half, 1 if interleaved else 0, wd, qp, kp, cos.data_ptr(), sin.data_ptr(), rows, pos, eps)
 
 
-def _ref(h):
-    return None if h is None else ctypes.byref(h)
+def _out_heads(out, like, dim, dev, what):
+    """An output of `like`'s shape (a new tensor when None) and its mx_heads."""
+    if out is None:
+        out = torch.empty_like(like, memory_format=torch.contiguous_format)
+    elif out.shape != like.shape:
+        raise ValueError(f"{what}: expected the shape {tuple(like.shape)}")
+    return out, _heads(out, dim, dev, what)
 
 
 def mx_qk_rope(q, k, cos, sin, positions, q_weight=None, k_weight=None, eps=1e-6, interleaved=False, q_out=None,
@@ -483,22 +502,25 @@ def mx_qk_rope(q, k, cos, sin, positions, q_weight=None, k_weight=None, eps=1e-6
     pairs (2i, 2i+1) instead of (i, i + rot_dim/2).  q_out, k_out: tensors to
     write into (q and k themselves included), else new ones.
     Returns (q_out, k_out)."""
-    _need(q.dim() == 3, "mx_qk_rope: q must be tokens x heads x dim")
-    dev, dim = q.device, q.shape[2]
+    if q.dim() != 3:
+        raise ValueError("mx_qk_rope: q must be tokens x heads x dim")
+    dev, dim = q.get_device(), q.size(2)
     r = _rope_args(q, k, cos, sin, positions, q_weight, k_weight, eps, interleaved, "mx_qk_rope")
-    if q_out is None:
-        q_out = torch.empty(q.shape, dtype=q.dtype, device=dev)
-    hq, ho = _heads(q, dim, dev, "q"), _heads(q_out, dim, dev, "q_out")
-    _need(q_out.shape[0] == q.shape[0], "mx_qk_rope: q_out must have q's shape")
-    hk = hp = None
+    hq = _heads(q, dim, dev, "mx_qk_rope: q")
+    q_out, oq = _out_heads(q_out, q, dim, dev, "mx_qk_rope: q_out")
+    hk = ok = None
     if k is not None:
-        if k_out is None:
-            k_out = torch.empty(k.shape, dtype=k.dtype, device=dev)
-        hk, hp = _heads(k, dim, dev, "k"), _heads(k_out, dim, dev, "k_out")
-        _need(k_out.shape[0] == k.shape[0], "mx_qk_rope: k_out must have k's shape")
-    _check(lib().mx_qk_rope(ctypes.byref(r), ctypes.byref(hq), _ref(hk), ctypes.byref(ho), _ref(hp), _stream_ptr(stream)),
-           "mx_qk_rope")
+        hk = _heads(k, dim, dev, "mx_qk_rope: k")
+        k_out, ok = _out_heads(k_out, k, dim, dev, "mx_qk_rope: k_out")
+    _check(lib().mx_qk_rope(r, hq, hk, oq, ok, _stream_ptr(stream)), "mx_qk_rope")
     return q_out, k_out
+
+
+def mx_qk_rope_workspace_size(tokens, dim, rot_dim, weights=True):
+    """Workspace bytes of mx_qk_rope_backward (0 without norm weights)."""
+    a = 256 if weights else 0                  # any aligned address: only whether it is set counts here
+    r = _PACK_ROPE(tokens, dim, rot_dim, 0, DTYPE_F32, a, a, 256, 256, 1, 256, 0.0)
+    return int(lib().mx_qk_rope_workspace_size(r))
 
 
 def mx_qk_rope_backward(dy_q, dy_k, q, k, cos, sin, positions, q_weight=None, k_weight=None, eps=1e-6,
@@ -506,37 +528,33 @@ def mx_qk_rope_backward(dy_q, dy_k, q, k, cos, sin, positions, q_weight=None, k_
     """Gradient of mx_qk_rope: dy_q, dy_k are the gradients of its outputs, the
     rest are its arguments.  Returns (dq, dk, dq_weight, dk_weight); the weight
     gradients are fp32 (None without that weight).  dq, dk may be dy_q, dy_k."""
-    _need(q.dim() == 3, "mx_qk_rope_backward: q must be tokens x heads x dim")
-    dev, dim = q.device, q.shape[2]
+    if q.dim() != 3 or (k is None) != (dy_k is None):
+        raise ValueError("mx_qk_rope_backward: q must be tokens x heads x dim, and dy_k and k go together")
+    dev, dim = q.get_device(), q.size(2)
     r = _rope_args(q, k, cos, sin, positions, q_weight, k_weight, eps, interleaved, "mx_qk_rope_backward")
-    _need((k is None) == (dy_k is None), "mx_qk_rope_backward: dy_k and k go together")
-    sets = []
-    for y, x, d in ((dy_q, q, dq), (dy_k, k, dk)):
-        if x is None:
-            sets.append((None, None, None, None))
-            continue
-        if d is None:
-            d = torch.empty(x.shape, dtype=x.dtype, device=dev)
-        _need(y.shape == x.shape and d.shape == x.shape, "mx_qk_rope_backward: gradients must have their heads' shape")
-        sets.append((d, _heads(y, dim, dev, "dy"), _heads(x, dim, dev, "x"), _heads(d, dim, dev, "dx")))
-    dws = [None if w is None else torch.empty(dim, dtype=torch.float32, device=dev) for w in (q_weight, k_weight)]
-    need = lib().mx_qk_rope_workspace_size(ctypes.byref(r))
-    if workspace is None and need:
-        workspace = _empty(need, dev)
-    (dq, gq, xq, oq), (dk, gk, xk, ok) = sets
-    rc = lib().mx_qk_rope_backward(ctypes.byref(r), ctypes.byref(gq), _ref(gk), ctypes.byref(xq), _ref(xk), ctypes.byref(oq),
-                                   _ref(ok), _raw(dws[0]), _raw(dws[1]), _raw(workspace),
-                                   0 if workspace is None else workspace.numel(), _stream_ptr(stream))
-    _check(rc, "mx_qk_rope_backward")
-    return dq, dk, dws[0], dws[1]
+    if dy_q.shape != q.shape or (k is not None and dy_k.shape != k.shape):
+        raise ValueError("mx_qk_rope_backward: gradients must have their heads' shape")
+    gq, xq = _heads(dy_q, dim, dev, "mx_qk_rope_backward: dy_q"), _heads(q, dim, dev, "mx_qk_rope_backward: q")
+    dq, oq = _out_heads(dq, q, dim, dev, "mx_qk_rope_backward: dq")
+    gk = xk = ok = None
+    if k is not None:
+        gk, xk = _heads(dy_k, dim, dev, "mx_qk_rope_backward: dy_k"), _heads(k, dim, dev, "mx_qk_rope_backward: k")
+        dk, ok = _out_heads(dk, k, dim, dev, "mx_qk_rope_backward: dk")
+    dqw = None if q_weight is None else cos.new_empty((dim,))
+    dkw = None if k_weight is None else cos.new_empty((dim,))
+    if workspace is None and (dqw is not None or dkw is not None):
+        workspace = _empty(lib().mx_qk_rope_workspace_size(r), q.device)
+    _check(lib().mx_qk_rope_backward(r, gq, gk, xq, xk, oq, ok, _raw(dqw), _raw(dkw), _raw(workspace),
+                                     0 if workspace is None else workspace.numel(), _stream_ptr(stream)), "mx_qk_rope_backward")
+    return dq, dk, dqw, dkw
 
 
-@dataclass
+@dataclass(frozen=True)
 class KVCache:
     """A paged cache of keys and values.  fmt None: k and v are bf16, pages x
     heads x page_size x dim.  fmt MXFP8_E4M3 or MXFP4: uint8 codes, pages x
     heads x page_size x (dim or dim/2), with uint8 E8M0 scales pages x heads x
-    page_size x dim/32."""
+    page_size x dim/32.  Fixed once made: its C struct is packed here."""
     fmt: Format
     k: torch.Tensor
     v: torch.Tensor
@@ -545,23 +563,33 @@ class KVCache:
 
     def __post_init__(self):
         bits = 16 if self.fmt is None else {ELEM_FP8_E4M3: 8, ELEM_E2M1: 4}.get(self.fmt.elem)
-        _need(bits is not None, "KVCache: the format must have E4M3 or E2M1 elements")
-        dt = torch.bfloat16 if self.fmt is None else torch.uint8
-        _need(self.k.dim() == 4 and self.v.shape == self.k.shape, "KVCache: k and v must be pages x heads x page_size x dim")
-        self.pages, self.heads, self.page_size, last = self.k.shape
-        self.dim = last * 2 if bits == 4 else last
-        need = [(self.k, self.k.shape, dt), (self.v, self.k.shape, dt)]
+        if bits is None:
+            raise ValueError("KVCache: the format must have E4M3 or E2M1 elements")
+        if self.k.dim() != 4:
+            raise ValueError("KVCache: k must be pages x heads x page_size x dim")
+        put = lambda name, v: object.__setattr__(self, name, v)
+        pages, heads, page_size, last = self.k.shape
+        dim = last * 2 if bits == 4 else last
+        dtype = torch.bfloat16 if self.fmt is None else torch.uint8
+        need = [(self.k, self.k.shape, dtype), (self.v, self.k.shape, dtype)]
         if self.fmt is not None:
-            grid = (*self.k.shape[:3], self.dim // 32)
+            grid = (pages, heads, page_size, dim // 32)
             need += [(self.k_scales, grid, torch.uint8), (self.v_scales, grid, torch.uint8)]
-        for t, shape, dtype in need:
-            _need(t is not None and t.shape == shape and t.dtype == dtype and t.is_contiguous() and t.device == self.k.device,
-                  f"KVCache: expected a contiguous {dtype} buffer of {tuple(shape)}")
+        for t, shape, dt in need:
+            if t is None or t.shape != shape or t.dtype != dt or not t.is_contiguous() or t.device != self.k.device:
+                raise ValueError(f"KVCache: expected a contiguous {dt} buffer of {tuple(shape)}")
+        for name, v in (("pages", pages), ("heads", heads), ("page_size", page_size), ("dim", dim)):
+            put(name, v)
+        f = None if self.fmt is None else self.fmt.c()
+        put("_format", f)
+        c = MxKVCache(None if f is None else ctypes.pointer(f), self.k.data_ptr(), self.v.data_ptr(),
+                      None if f is None else self.k_scales.data_ptr(), None if f is None else self.v_scales.data_ptr(), pages,
+                      page_size, heads, dim)
+        put("_c", c)
+        put("_ref", ctypes.byref(c))
 
     def c(self):
-        f = None if self.fmt is None else ctypes.pointer(self.fmt.c())
-        return MxKVCache(f, self.k.data_ptr(), self.v.data_ptr(), _raw(self.k_scales), _raw(self.v_scales), self.pages,
-                         self.page_size, self.heads, self.dim)
+        return self._c
 
 
 def alloc_kv_cache(fmt, pages, page_size, heads, dim, device="cuda"):
@@ -578,20 +606,18 @@ def mx_cache_write(cache: KVCache, k, v, slots, stream=None):
     fp32, any token and head strides) to the cache, quantized to its format.
     slots: int64 per token, page * page_size + position in the page; a slot
     outside the cache skips its token.  Returns the cache."""
-    dev = cache.k.device
-    hk, hv = _heads(k, cache.dim, dev, "k"), _heads(v, cache.dim, dev, "v")
-    tokens = k.shape[0]
-    _need(v.shape[0] == tokens, "mx_cache_write: k and v differ in tokens")
-    _need(slots.shape == (tokens,) and slots.dtype == torch.int64 and slots.is_contiguous() and slots.device == dev,
-          f"mx_cache_write: slots must be {tokens} contiguous int64")
-    rc = lib().mx_cache_write(ctypes.byref(cache.c()), ctypes.byref(hk), ctypes.byref(hv), tokens, slots.data_ptr(),
-                              _stream_ptr(stream))
-    _check(rc, "mx_cache_write")
+    dev, dim = cache.k.get_device(), cache.dim
+    hk, hv = _heads(k, dim, dev, "mx_cache_write: k"), _heads(v, dim, dev, "mx_cache_write: v")
+    tokens = k.size(0)
+    if v.size(0) != tokens:
+        raise ValueError("mx_cache_write: k and v differ in tokens")
+    at = _vector(slots, tokens, torch.int64, dev, "mx_cache_write: slots")
+    _check(lib().mx_cache_write(cache._ref, hk, hv, tokens, at, _stream_ptr(stream)), "mx_cache_write")
     return cache
 
 
 def mx_attend_workspace_size(cache: KVCache, batch, q_heads, table_cols):
-    return int(lib().mx_attend_workspace_size(ctypes.byref(cache.c()), batch, q_heads, table_cols))
+    return int(lib().mx_attend_workspace_size(cache._ref, batch, q_heads, table_cols))
 
 
 def alloc_attend_workspace(cache: KVCache, batch, q_heads, table_cols):
@@ -606,31 +632,25 @@ def mx_attend(q, cache: KVCache, page_table, lengths, scale=None, out=None, lse=
     (allocate) or a batch x heads fp32 tensor.  workspace: as
     alloc_attend_workspace gives (allocated when None).
     Returns out, or (out, lse) when lse is asked for."""
-    _need(q.dim() == 3, "mx_attend: q must be batch x heads x dim")
-    dev = cache.k.device
-    batch, heads, dim = q.shape
-    hq = _heads(q, cache.dim, dev, "q")
-    _need(page_table.dim() == 2 and page_table.shape[0] == batch and page_table.dtype == torch.int32 and
-          page_table.device == dev and (page_table.numel() == 0 or page_table.stride(1) == 1),
-          f"mx_attend: page_table must be {batch} rows of contiguous int32")
-    _need(lengths.shape == (batch,) and lengths.dtype == torch.int32 and lengths.is_contiguous() and lengths.device == dev,
-          f"mx_attend: lengths must be {batch} contiguous int32")
-    if out is None:
-        out = torch.empty((batch, heads, dim), dtype=q.dtype, device=dev)
-    ho = _heads(out, cache.dim, dev, "out")
-    _need(out.shape[0] == batch, "mx_attend: out must have q's shape")
+    dev, dim = cache.k.get_device(), cache.dim
+    hq = _heads(q, dim, dev, "mx_attend: q")
+    batch, heads = q.size(0), q.size(1)
+    if page_table.dim() != 2 or page_table.dtype != torch.int32 or page_table.size(0) != batch or page_table.get_device() != dev:
+        raise ValueError(f"mx_attend: page_table must be {batch} rows of int32 on the cache's device")
+    cols = page_table.size(1)
+    stride, last = page_table.stride()
+    if last != 1 and cols > 1 and batch:
+        raise ValueError("mx_attend: the rows of page_table must be contiguous")
+    n = _vector(lengths, batch, torch.int32, dev, "mx_attend: lengths")
+    out, ho = _out_heads(out, q, dim, dev, "mx_attend: out")
     if lse is True:
-        lse = torch.empty((batch, heads), dtype=torch.float32, device=dev)
-    elif lse is not None:
-        _need(lse.shape == (batch, heads) and lse.dtype == torch.float32 and lse.is_contiguous() and lse.device == dev,
-              f"mx_attend: lse must be a contiguous fp32 {batch} x {heads}")
-    c = cache.c()
-    cols = page_table.shape[1]
+        lse = torch.empty((batch, heads), dtype=torch.float32, device=q.device)
+    elif lse is not None and (lse.shape != (batch, heads) or lse.dtype != torch.float32 or not lse.is_contiguous() or
+                              lse.get_device() != dev):
+        raise ValueError(f"mx_attend: lse must be a contiguous fp32 {batch} x {heads}")
     if workspace is None:
-        workspace = _empty(lib().mx_attend_workspace_size(ctypes.byref(c), batch, heads, cols), dev)
-    rc = lib().mx_attend(ctypes.byref(c), ctypes.byref(hq), batch, page_table.data_ptr(), cols,
-                         cols if batch <= 1 else page_table.stride(0), lengths.data_ptr(),
-                         dim ** -0.5 if scale is None else scale, ctypes.byref(ho), _raw(lse), workspace.data_ptr(),
-                         workspace.numel(), _stream_ptr(stream))
-    _check(rc, "mx_attend")
+        workspace = _empty(lib().mx_attend_workspace_size(cache._ref, batch, heads, cols), q.device)
+    _check(lib().mx_attend(cache._ref, hq, batch, page_table.data_ptr(), cols, cols if batch <= 1 else stride, n,
+                           dim ** -0.5 if scale is None else scale, ho, _raw(lse), workspace.data_ptr(), workspace.numel(),
+                           _stream_ptr(stream)), "mx_attend")
     return out if lse is None else (out, lse)

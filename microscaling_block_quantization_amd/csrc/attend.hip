@@ -34,6 +34,7 @@ namespace {
 
 typedef __bf16 bf8v __attribute__((ext_vector_type(8)));
 typedef __bf16 bf2v __attribute__((ext_vector_type(2)));
+typedef float f2v __attribute__((ext_vector_type(2)));
 typedef float f4v __attribute__((ext_vector_type(4)));
 typedef short s2v __attribute__((ext_vector_type(2)));
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
@@ -133,9 +134,9 @@ __global__ __launch_bounds__(CT) void k_cache_write(CacheWrite p) {
 // ---------------------------------------------------------------------------
 // Attention
 // ---------------------------------------------------------------------------
-constexpr int AW = 4, AT = 64 * AW;    // waves, threads
 constexpr int TILE = 32;               // tokens a wave takes at a time
 constexpr int QH = 16;                 // query heads of one workgroup
+constexpr int EIGHT_MAX = 128;         // largest head dimension whose registers leave room for eight waves
 
 // Bits of one value, and the widest run of the head dimension (a "unit") that
 // 4 lanes of a token cover with one load of at most 16 bytes each.
@@ -198,28 +199,40 @@ __device__ __forceinline__ void each_(F&& f, seq<I...>) { (f(ic<I>{}), ...); }
 template <int N, typename F>
 __device__ __forceinline__ void each(F&& f) { each_(f, typename make_seq<N>::type{}); }
 
-// a query value as its exact bf16 parts
-__device__ __forceinline__ void parts_of(float x, uint32_t (&o)[3]) {
+// a query value as its exact bf16 parts (bits in the upper halves)
+struct Parts {
+    uint32_t h, m, l;
+};
+__device__ __forceinline__ Parts parts_of(float x) {
     const uint32_t u = fbits(x);
-    if ((u & 0x7f800000u) == 0x7f800000u) {
-        o[0] = bf16_rne(x);
-        o[1] = o[2] = 0;
-        return;
-    }
+    if ((u & 0x7f800000u) == 0x7f800000u) return Parts{(uint32_t)bf16_rne(x) << 16, 0u, 0u};
     const float r = x - bitsf(u & 0xffff0000u);
-    o[0] = u >> 16;
-    o[1] = fbits(r) >> 16;
-    o[2] = fbits(r - bitsf(fbits(r) & 0xffff0000u)) >> 16;
+    return Parts{u & 0xffff0000u, fbits(r) & 0xffff0000u, fbits(r - bitsf(fbits(r) & 0xffff0000u)) & 0xffff0000u};
 }
+__device__ __forceinline__ uint32_t pack_hi(uint32_t a, uint32_t b) { return __builtin_amdgcn_perm(b, a, 0x07060302u); }
 
-template <int D, int KIND, bool QF32, bool PAGE16>
-__global__ __launch_bounds__(AT) void k_attend(AttendParams p) {
+// Left to itself the scheduler moves loads behind the wait for older ones.
+#define ISSUED __builtin_amdgcn_sched_barrier(0)
+
+// One wave takes every AW-th tile of 32 tokens of the workgroup's chunk.  The
+// loads of a tile's values go out before its scores are formed, those of the
+// next tile's keys before its second product, so one of the two is always in
+// flight; quantized tiles are small, and all of the next one's loads go out
+// before the scores.  PAGE16: pages of a multiple of 16 tokens, so that 16 tokens share a
+// page, whose number is then one scalar load, and reading all 16 stays inside
+// the page whatever the length.
+template <int D, int KIND, bool QF32, bool PAGE16, int AW>
+__global__ __launch_bounds__(64 * AW, D <= 128 ? 2 : 1) void k_attend(AttendParams p) {
     constexpr int QP = QF32 ? 3 : 1;              // bf16 parts of a query
     constexpr int PP = QF32 ? 3 : 2;              // bf16 parts of a probability
-    constexpr int BITS = kind_bits(KIND), ROWB = D * BITS / 8;
+    constexpr int BITS = kind_bits(KIND), ROWB = D * BITS / 8, NB = D / 32;
     constexpr int KU = count_units(D, unit_max(KIND));     // units of the score product
     constexpr int VU = count_units(D, 128);                // runs of 16 lanes of the second product
     constexpr int LD = D + 1;                              // LDS row of one head's sums
+    // a quantized tile is small enough to hold the next one's keys and values too
+    constexpr bool FAR = KIND != KV_BF16 && PAGE16 && D <= 128 && !QF32;
+    // scales of a token (and of the value operand's four tokens) as whole dwords
+    constexpr bool WIDE_SC = KIND != KV_BF16 && PAGE16 && (D == 64 || D % 128 == 0);
     extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
 
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -242,9 +255,97 @@ __global__ __launch_bounds__(AT) void k_attend(AttendParams p) {
     const int len = (int)len64, t0 = split * p.chunk;
     if (t0 >= len && !(len == 0 && split == 0)) return;    // nothing here; the join does not read it
     const int tend = len < t0 + p.chunk ? len : t0 + p.chunk;
+    const int32_t* table = p.table + b * p.table_stride;
+
+    bool bad = false;
+    // cache row of token t (page lookup); a bad page reads page 0
+    auto row_of = [&](int t) -> int64_t {
+        const uint32_t pg = (uint32_t)(((uint64_t)(uint32_t)t * p.page_mul) >> p.page_shift);
+        int64_t n = table[pg];
+        if (n < 0 || n >= p.c.pages) { n = 0; bad = true; }
+        return (n * p.c.heads + kvh) * p.c.page + (t - (int)pg * p.c.page);
+    };
+    // rows of the operands of the tile at tb: keys 16 h + r, values 16 h + 4 g + i
+    struct Place {
+        int64_t base[2];           // PAGE16: the row of token 16 h
+        int64_t k[PAGE16 ? 1 : 2], v[PAGE16 ? 1 : 2][4];
+    };
+    auto place = [&](Place& o, int tb) {
+#pragma unroll
+        for (int h = 0; h < 2; h++) {
+            if constexpr (PAGE16) {
+                o.base[h] = row_of(tb + 16 * h < tend ? tb + 16 * h : tb);
+            } else {
+                const int tk = tb + 16 * h + r;
+                o.k[h] = row_of(tk < tend ? tk : tend - 1);
+#pragma unroll
+                for (int i = 0; i < 4; i++) {
+                    const int t = tb + 16 * h + 4 * g + i;
+                    o.v[h][i] = row_of(t < tend ? t : tend - 1);
+                }
+            }
+        }
+    };
+    // bytes `at` of key row 16 h + r / value row 16 h + 4 g + i of an array of `per` bytes a row
+    auto key_at = [&](const uint8_t* a, const Place& o, int h, int per, uint32_t at) -> const uint8_t* {
+        if constexpr (PAGE16) return a + o.base[h] * per + (uint32_t)(r * per + at);
+        else return a + o.k[h] * per + at;
+    };
+    auto value_at = [&](const uint8_t* a, const Place& o, int h, int i, int per, uint32_t at) -> const uint8_t* {
+        if constexpr (PAGE16) return a + o.base[h] * per + (uint32_t)((4 * g + i) * per + at);
+        else return a + o.v[h][i] * per + at;
+    };
+
+    // a tile's keys: 16-byte pieces by unit, and their scales
+    struct Keys {
+        uint32_t w[2][KU][4], sc[2][KIND == KV_BF16 ? 1 : WIDE_SC ? (NB + 3) / 4 : KU];
+    };
+    auto load_keys = [&](Keys& o, const Place& at) {
+#pragma unroll
+        for (int h = 0; h < 2; h++) {
+            each<KU>([&](auto iu) {
+                constexpr int BASE = unit_base(D, unit_max(KIND), iu.value), U = unit_at(D, BASE, unit_max(KIND));
+                load_bytes<U * BITS / 32>(o.w[h][iu.value], key_at(p.c.k, at, h, ROWB, (BASE + g * (U / 4)) * BITS / 8));
+                if constexpr (KIND != KV_BF16 && !WIDE_SC)
+                    o.sc[h][iu.value] = *key_at(p.c.ks, at, h, NB, (BASE + g * (U / 4)) / 32);
+            });
+            if constexpr (WIDE_SC) load_bytes<NB>(o.sc[h], key_at(p.c.ks, at, h, NB, 0));
+        }
+    };
+    // its values: runs of W per token, and their scales
+    struct Values {
+        uint32_t w[VU][8][4], sc[WIDE_SC ? 2 : VU][WIDE_SC ? NB : 8];
+    };
+    auto load_values = [&](Values& o, const Place& at) {
+        each<VU>([&](auto iu) {
+            constexpr int BASE = unit_base(D, 128, iu.value), W = unit_at(D, BASE, 128) / 16;
+#pragma unroll
+            for (int i = 0; i < 8; i++) {
+                load_bytes<W * BITS / 8>(o.w[iu.value][i], value_at(p.c.v, at, i / 4, i % 4, ROWB, (BASE + r * W) * BITS / 8));
+                if constexpr (KIND != KV_BF16 && !WIDE_SC)
+                    o.sc[iu.value][i] = *value_at(p.c.vs, at, i / 4, i % 4, NB, (BASE + r * W) / 32);
+            }
+        });
+        if constexpr (WIDE_SC) {
+            // four tokens' scales, NB dwords
+#pragma unroll
+            for (int h = 0; h < 2; h++)
+#pragma unroll
+                for (int k = 0; k < NB; k += 4) load_bytes<(NB < 4 ? NB : 4) * 4>(&o.sc[h][k], value_at(p.c.vs, at, h, 0, NB, 4 * k));
+        }
+    };
+
+    Place here, then;
+    Keys keys;
+    const int first = t0 + wave * TILE;
+    if (first < tend) {
+        place(here, first);
+        load_keys(keys, here);
+    }
+    ISSUED;
 
     // the query, laid out as the score product's columns
-    uint32_t q[QP][D / 32][4];
+    uint32_t q[QP][NB][4];
     {
         const int64_t at = b * p.q_ts + (int64_t)(h0 + (r < nh ? r : nh - 1)) * p.q_hs;
         each<KU>([&](auto iu) {
@@ -255,11 +356,11 @@ __global__ __launch_bounds__(AT) void k_attend(AttendParams p) {
                 if constexpr (QF32) {
 #pragma unroll
                     for (int e = 0; e < 4; e++) {
-                        uint32_t x[3], y[3];
-                        parts_of(static_cast<const float*>(p.q)[d + 2 * e], x);
-                        parts_of(static_cast<const float*>(p.q)[d + 2 * e + 1], y);
-#pragma unroll
-                        for (int k = 0; k < 3; k++) q[k][BASE / 32 + f][e] = x[k] | y[k] << 16;
+                        const Parts x = parts_of(static_cast<const float*>(p.q)[d + 2 * e]);
+                        const Parts y = parts_of(static_cast<const float*>(p.q)[d + 2 * e + 1]);
+                        q[0][BASE / 32 + f][e] = pack_hi(x.h, y.h);
+                        q[QP - 2][BASE / 32 + f][e] = pack_hi(x.m, y.m);
+                        q[QP - 1][BASE / 32 + f][e] = pack_hi(x.l, y.l);
                     }
                 } else {
                     load_bytes<16>(q[0][BASE / 32 + f], reinterpret_cast<const uint8_t*>(static_cast<const uint16_t*>(p.q) + d));
@@ -272,54 +373,32 @@ __global__ __launch_bounds__(AT) void k_attend(AttendParams p) {
 #pragma unroll
     for (int i = 0; i < D / 16; i++) acc[i] = f4v{0.f, 0.f, 0.f, 0.f};
     float m = -INFINITY, l = 0.f;                          // of head r; l: this lane's tokens
-    bool bad = false;
     const float zs = p.scale * 1.44269504088896340736f;
-    const int32_t* table = p.table + b * p.table_stride;
 
-    // cache row of token t (page lookup); a bad page reads page 0
-    auto row_of = [&](int t) -> int64_t {
-        const uint32_t pg = (uint32_t)(((uint64_t)(uint32_t)t * p.page_mul) >> p.page_shift);
-        int64_t n = table[pg];
-        if (n < 0 || n >= p.c.pages) { n = 0; bad = true; }
-        return (n * p.c.heads + kvh) * p.c.page + (t - (int)pg * p.c.page);
-    };
-
-    for (int tb = t0 + wave * TILE; tb < tend; tb += AW * TILE) {
-        // rows of the key operand: token 16 h + r; of the value operand: 16 h + 4 g + i
-        int64_t kr[2], vr[2][4];
-#pragma unroll
-        for (int h = 0; h < 2; h++) {
-            if constexpr (PAGE16) {
-                // 16 tokens lie in one page
-                const int t = tb + 16 * h < tend ? tb + 16 * h : tb;
-                const int64_t base = row_of(t);
-                const int left = tend - 1 - t;             // last usable token from the base
-                kr[h] = base + (r < left ? r : left);
-#pragma unroll
-                for (int i = 0; i < 4; i++) vr[h][i] = base + (4 * g + i < left ? 4 * g + i : left);
-            } else {
-                const int tk = tb + 16 * h + r;
-                kr[h] = row_of(tk < tend ? tk : tend - 1);
-#pragma unroll
-                for (int i = 0; i < 4; i++) {
-                    const int t = tb + 16 * h + 4 * g + i;
-                    vr[h][i] = row_of(t < tend ? t : tend - 1);
-                }
-            }
+    // the tile at tb from (keys, val); the next one's loads
+    auto tile_step = [&](int tb, Keys& keys, Values& val, Keys& next_keys, Values& next_val) {
+        if constexpr (!FAR) load_values(val, here);
+        const int next = tb + AW * TILE < tend ? tb + AW * TILE : tb;      // after the last tile: the same again, unused
+        place(then, next);
+        if constexpr (FAR) {
+            load_keys(next_keys, then);
+            load_values(next_val, then);
         }
+        ISSUED;
 
         // scores
         f4v z[2];
 #pragma unroll
         for (int h = 0; h < 2; h++) {
             z[h] = f4v{0.f, 0.f, 0.f, 0.f};
-            const uint8_t* krow = p.c.k + kr[h] * ROWB;
             each<KU>([&](auto iu) {
                 constexpr int BASE = unit_base(D, unit_max(KIND), iu.value), U = unit_at(D, BASE, unit_max(KIND));
-                uint32_t w[4];
-                load_bytes<U * BITS / 32>(w, krow + (BASE + g * (U / 4)) * BITS / 8);
+                const uint32_t* w = keys.w[h][iu.value];
                 float s = 1.f;
-                if constexpr (KIND != KV_BF16) s = e8m0(p.c.ks[kr[h] * (D / 32) + (BASE + g * (U / 4)) / 32]);
+                if constexpr (WIDE_SC)
+                    s = e8m0((keys.sc[h][BASE / 128] >> (BASE % 128 / 4)) >> (8 * (g * (U / 4) / 32)) & 0xffu);
+                else if constexpr (KIND != KV_BF16)
+                    s = e8m0(keys.sc[h][iu.value]);
                 each<U / 32>([&](auto fi) {
                     constexpr int f = fi.value;
                     const bf8v a = frag(pair_of<KIND, 4 * f>(w, s), pair_of<KIND, 4 * f + 1>(w, s),
@@ -331,6 +410,11 @@ __global__ __launch_bounds__(AT) void k_attend(AttendParams p) {
                     }
                 });
             });
+        }
+        if constexpr (!FAR) {
+            ISSUED;
+            load_keys(next_keys, then);
+            ISSUED;
         }
 
         // softmax of this lane's 8 tokens of head r
@@ -345,44 +429,46 @@ __global__ __launch_bounds__(AT) void k_attend(AttendParams p) {
             }
         zmax = fmaxf(zmax, __shfl_xor(zmax, 16, 64));
         zmax = fmaxf(zmax, __shfl_xor(zmax, 32, 64));
-        const float mn = fmaxf(m, zmax);
-        const float ms = mn == -INFINITY ? 0.f : mn;       // every score so far is -inf
-        const float grow = exp2f(m - ms);
-        m = mn;
-        l *= grow;
-        uint32_t pw[PP][4];                                // probabilities as bf16 pairs
-        float pr[8];
+        if (__any(zmax > m)) {                             // the maximum of some head grows
+            const float mn = fmaxf(m, zmax);
+            const float grow = exp2f(m - (mn == -INFINITY ? 0.f : mn));
+            m = mn;
+            l *= grow;
 #pragma unroll
-        for (int i = 0; i < 8; i++) {
-            pr[i] = exp2f(z[i / 4][i % 4] - ms);
-            l += pr[i];
+            for (int i = 0; i < D / 16; i++) acc[i] *= grow;
         }
+        const float ms = m == -INFINITY ? 0.f : m;         // every score so far is -inf
+        uint32_t pw[PP][4];                                // probabilities as bf16 pairs
 #pragma unroll
         for (int i = 0; i < 4; i++) {
-            float x = pr[2 * i], y = pr[2 * i + 1];
+            float x = exp2f(z[i / 2][2 * (i % 2)] - ms), y = exp2f(z[i / 2][2 * (i % 2) + 1] - ms);
+            l += x + y;
 #pragma unroll
             for (int k = 0; k < PP; k++) {
-                const uint32_t a = bf16_rne(x), c = bf16_rne(y);
-                pw[k][i] = a | c << 16;
-                x -= bitsf(a << 16);
-                y -= bitsf(c << 16);
+                const f2v xy = {x, y};
+                pw[k][i] = bits_of(__builtin_convertvector(xy, bf2v));
+                x -= bitsf(pw[k][i] << 16);
+                y -= bitsf(pw[k][i] & 0xffff0000u);
             }
         }
-#pragma unroll
-        for (int i = 0; i < D / 16; i++) acc[i] *= grow;
 
         // sums of p v
         const bool part = tb + TILE > tend;
         each<VU>([&](auto iu) {
             constexpr int BASE = unit_base(D, 128, iu.value), W = unit_at(D, BASE, 128) / 16;
-            constexpr int WB = W * BITS / 8;               // bytes a lane reads per token
-            uint32_t v[8][WB < 4 ? 1 : WB / 4];
+            constexpr int WD = W * BITS / 8 < 4 ? 1 : W * BITS / 32;
             float s[8];
 #pragma unroll
             for (int i = 0; i < 8; i++) {
-                load_bytes<WB>(v[i], p.c.v + vr[i / 4][i % 4] * ROWB + (BASE + r * W) * BITS / 8);
-                if constexpr (KIND != KV_BF16) s[i] = e8m0(p.c.vs[vr[i / 4][i % 4] * (D / 32) + (BASE + r * W) / 32]);
-                else s[i] = 1.f;
+                if constexpr (WIDE_SC) {
+                    constexpr int NBW = NB;
+                    const int n = (i % 4) * NBW + BASE / 32;               // byte of the first of this run's blocks
+                    s[i] = e8m0((val.sc[i / 4][n / 4] >> (8 * (n % 4))) >> (8 * (r * W / 32)) & 0xffu);
+                } else if constexpr (KIND != KV_BF16) {
+                    s[i] = e8m0(val.sc[iu.value][i]);
+                } else {
+                    s[i] = 1.f;
+                }
             }
             if (part) {
                 // past the end: whatever the cache holds is taken as zero
@@ -391,14 +477,14 @@ __global__ __launch_bounds__(AT) void k_attend(AttendParams p) {
                     if (tb + 16 * (i / 4) + 4 * g + i % 4 >= tend) {
                         s[i] = 1.f;
 #pragma unroll
-                        for (int k = 0; k < (WB < 4 ? 1 : WB / 4); k++) v[i][k] = 0u;
+                        for (int k = 0; k < WD; k++) val.w[iu.value][i][k] = 0u;
                     }
             }
             each<W / 2>([&](auto pi) {
                 constexpr int I = pi.value;
                 uint32_t t[8];
 #pragma unroll
-                for (int i = 0; i < 8; i++) t[i] = pair_of<KIND, I>(v[i], s[i]);
+                for (int i = 0; i < 8; i++) t[i] = pair_of<KIND, I>(val.w[iu.value][i], s[i]);
 #pragma unroll
                 for (int odd = 0; odd < 2; odd++) {
                     const uint32_t sel = odd ? 0x07060302u : 0x05040100u;
@@ -411,6 +497,22 @@ __global__ __launch_bounds__(AT) void k_attend(AttendParams p) {
                 }
             });
         });
+        here = then;
+    };
+    if constexpr (FAR) {
+        Keys keys2;
+        Values val, val2;
+        if (first < tend) load_values(val, here);
+        for (int tb = first; tb < tend; tb += 2 * AW * TILE) {
+            tile_step(tb, keys, val, keys2, val2);
+            if (tb + AW * TILE >= tend) break;
+            tile_step(tb + AW * TILE, keys2, val2, keys, val);
+        }
+    } else {
+        for (int tb = first; tb < tend; tb += AW * TILE) {
+            Values val;
+            tile_step(tb, keys, val, keys, val);
+        }
     }
 
     // the waves' triples, joined through LDS
@@ -418,31 +520,32 @@ __global__ __launch_bounds__(AT) void k_attend(AttendParams p) {
     l += __shfl_xor(l, 32, 64);
     if (__any(bad)) l = bitsf(0x7fc00000u);
     float* sums = reinterpret_cast<float*>(smem);                  // [wave][head][LD]
-    float* ml = sums + AW * QH * LD;                               // [wave][head][2]
-    each<VU>([&](auto iu) {
-        constexpr int BASE = unit_base(D, 128, iu.value), W = unit_at(D, BASE, 128) / 16;
+    float* ml = sums + AW * nh * LD;                               // [wave][head][2]
+    if (r < nh) {
+        each<VU>([&](auto iu) {
+            constexpr int BASE = unit_base(D, 128, iu.value), W = unit_at(D, BASE, 128) / 16;
 #pragma unroll
-        for (int i = 0; i < W; i++)
+            for (int i = 0; i < W; i++)
 #pragma unroll
-            for (int e = 0; e < 4; e++)
-                sums[(wave * QH + r) * LD + BASE + (4 * g + e) * W + i] = acc[BASE / 16 + i][e];
-    });
-    if (g == 0) {
-        ml[(wave * QH + r) * 2] = m;
-        ml[(wave * QH + r) * 2 + 1] = l;
+                for (int e = 0; e < 4; e++) sums[(wave * nh + r) * LD + BASE + (4 * g + e) * W + i] = acc[BASE / 16 + i][e];
+        });
+        if (g == 0) {
+            ml[(wave * nh + r) * 2] = m;
+            ml[(wave * nh + r) * 2 + 1] = l;
+        }
     }
     __syncthreads();
-    for (int i = threadIdx.x; i < nh * D; i += AT) {
+    for (int i = threadIdx.x; i < nh * D; i += 64 * AW) {
         const int h = i / D, d = i - h * D;
         float M = -INFINITY, L = 0.f, o = 0.f;
 #pragma unroll
-        for (int w = 0; w < AW; w++) M = fmaxf(M, ml[(w * QH + h) * 2]);
+        for (int w = 0; w < AW; w++) M = fmaxf(M, ml[(w * nh + h) * 2]);
         const float Ms = M == -INFINITY ? 0.f : M;
 #pragma unroll
         for (int w = 0; w < AW; w++) {
-            const float f = exp2f(ml[(w * QH + h) * 2] - Ms);
-            L += f * ml[(w * QH + h) * 2 + 1];
-            o += f * sums[(w * QH + h) * LD + d];
+            const float f = exp2f(ml[(w * nh + h) * 2] - Ms);
+            L += f * ml[(w * nh + h) * 2 + 1];
+            o += f * sums[(w * nh + h) * LD + d];
         }
         const int64_t bh = b * p.q_heads + h0 + h;
         if (p.splits > 1) {
@@ -461,14 +564,16 @@ __global__ __launch_bounds__(AT) void k_attend(AttendParams p) {
         }
     }
 }
+#undef ISSUED
 
-// Joins the splits of one sequence and query head: a wave takes every fourth
-// split, lanes the head dimension.
+// Joins the splits of one sequence and query head: groups of D / 4 lanes (a
+// power of two of them) take every JG-th split, four values a lane, then their
+// triples are joined in order.
 template <int D, bool QF32>
 __global__ __launch_bounds__(256) void k_attend_join(AttendParams p) {
-    constexpr int N = (D + 63) / 64;
-    __shared__ float so[4][D], sl[4];
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    constexpr int LG = D <= 64 ? 16 : D <= 128 ? 32 : 64, JG = 256 / LG, AHEAD = 4;
+    __shared__ float so[JG][LG * 4], sm[JG], sl[JG];
+    const int grp = threadIdx.x / LG, u = threadIdx.x % LG;
     const int64_t bh = blockIdx.x, b = bh / p.q_heads;
     const int h = (int)(bh - b * p.q_heads);
     const int64_t cap = p.cols * p.c.page;
@@ -476,62 +581,88 @@ __global__ __launch_bounds__(256) void k_attend_join(AttendParams p) {
     len = len < 0 ? 0 : len > cap ? cap : len;
     int used = (int)((len + p.chunk - 1) / p.chunk);
     if (used < 1) used = 1;                          // an empty sequence's first workgroup leaves sum 0
-    const float* o = p.parts + bh * p.splits * D;
+    const float* o = p.parts + bh * p.splits * D + (4 * u < D ? 4 * u : 0);
     const float* x = p.parts + p.batch * p.q_heads * p.splits * D + bh * p.splits * 2;
-    float M = -INFINITY;
-    for (int i = lane; i < used; i += 64) M = fmaxf(M, x[2 * i]);
+    float M = -INFINITY, L = 0.f;
+    f4v v = {0.f, 0.f, 0.f, 0.f};
+    for (int i = grp; i < used; i += JG * AHEAD) {
+        f4v a[AHEAD];
+        float am[AHEAD], al[AHEAD];
 #pragma unroll
-    for (int k = 1; k < 64; k <<= 1) M = fmaxf(M, __shfl_xor(M, k, 64));
-    const float Ms = M == -INFINITY ? 0.f : M;
-    float v[N], L = 0.f;
+        for (int k = 0; k < AHEAD; k++) {
+            const int j = i + k * JG < used ? i + k * JG : i;
+            a[k] = *reinterpret_cast<const f4v*>(o + (int64_t)j * D);
+            am[k] = i + k * JG < used ? x[2 * j] : -INFINITY;
+            al[k] = x[2 * j + 1];
+        }
+        float Mn = M;
 #pragma unroll
-    for (int k = 0; k < N; k++) v[k] = 0.f;
-    for (int i = wave; i < used; i += 4) {
-        const float f = exp2f(x[2 * i] - Ms);
-        L += f * x[2 * i + 1];
+        for (int k = 0; k < AHEAD; k++) Mn = fmaxf(Mn, am[k]);
+        const float Ms = Mn == -INFINITY ? 0.f : Mn, old = exp2f(M - Ms);
+        L *= old;
+        v *= old;
 #pragma unroll
-        for (int k = 0; k < N; k++)
-            if (lane + 64 * k < D) v[k] += f * o[(int64_t)i * D + lane + 64 * k];
+        for (int k = 0; k < AHEAD; k++) {
+            if (i + k * JG >= used) break;
+            const float f = exp2f(am[k] - Ms);
+            L += f * al[k];
+            v += f * a[k];
+        }
+        M = Mn;
     }
-#pragma unroll
-    for (int k = 0; k < N; k++)
-        if (lane + 64 * k < D) so[wave][lane + 64 * k] = v[k];
-    if (lane == 0) sl[wave] = L;
+    *reinterpret_cast<f4v*>(&so[grp][4 * u]) = v;
+    if (u == 0) {
+        sm[grp] = M;
+        sl[grp] = L;
+    }
     __syncthreads();
-    L = sl[0] + sl[1] + sl[2] + sl[3];
-    for (int d = threadIdx.x; d < D; d += 256) {
-        const float s = so[0][d] + so[1][d] + so[2][d] + so[3][d];
-        const float r = L == 0.f ? 0.f : s / L;
+    if (threadIdx.x < D) {
+        const int d = threadIdx.x;
+        float Ma = -INFINITY, La = 0.f, s = 0.f;
+#pragma unroll
+        for (int k = 0; k < JG; k++) Ma = fmaxf(Ma, sm[k]);
+        const float Ms = Ma == -INFINITY ? 0.f : Ma;
+#pragma unroll
+        for (int k = 0; k < JG; k++) {
+            const float f = exp2f(sm[k] - Ms);
+            La += f * sl[k];
+            s += f * so[k][d];
+        }
+        const float r = La == 0.f ? 0.f : s / La;
         const int64_t at = b * p.o_ts + (int64_t)h * p.o_hs + d;
         if (QF32) static_cast<float*>(p.o)[at] = r;
         else static_cast<uint16_t*>(p.o)[at] = bf16_rne(r);
-        if (p.lse && d == 0) p.lse[bh] = L == 0.f ? -INFINITY : (Ms + log2f(L)) * 0.69314718055994530942f;
+        if (p.lse && d == 0) p.lse[bh] = La == 0.f ? -INFINITY : (Ms + log2f(La)) * 0.69314718055994530942f;
     }
 }
 
-template <int D, int KIND, bool QF32, bool PAGE16>
+template <int D, int KIND, bool QF32, bool PAGE16, int AW>
 hipError_t go(const AttendParams& p, hipStream_t s) {
-    const int group = p.q_heads / p.c.heads, tiles = (group + QH - 1) / QH;
+    const int group = p.q_heads / p.c.heads, tiles = (group + QH - 1) / QH, rows = group < QH ? group : QH;
     const int64_t n = p.batch * p.c.heads * tiles * p.splits;
-    constexpr int lds = (AW * QH * (D + 1) + AW * QH * 2) * (int)sizeof(float);
+    const int lds = AW * rows * (D + 3) * (int)sizeof(float);
     if (lds > 64 * 1024) {
-        const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(k_attend<D, KIND, QF32, PAGE16>),
+        const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(k_attend<D, KIND, QF32, PAGE16, AW>),
                                                  hipFuncAttributeMaxDynamicSharedMemorySize, lds);
         if (e != hipSuccess) return e;
     }
-    k_attend<D, KIND, QF32, PAGE16><<<(unsigned)n, AT, lds, s>>>(p);
+    k_attend<D, KIND, QF32, PAGE16, AW><<<(unsigned)n, 64 * AW, lds, s>>>(p);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess || p.splits == 1) return e;
     k_attend_join<D, QF32><<<(unsigned)(p.batch * p.q_heads), 256, 0, s>>>(p);
     return hipGetLastError();
 }
 
+template <int D, int KIND, bool QF32>
+hipError_t pages(const AttendParams& p, hipStream_t s) {
+    if constexpr (D <= EIGHT_MAX)
+        if (p.waves == 8) return p.c.page % 16 ? go<D, KIND, QF32, false, 8>(p, s) : go<D, KIND, QF32, true, 8>(p, s);
+    return p.c.page % 16 ? go<D, KIND, QF32, false, 4>(p, s) : go<D, KIND, QF32, true, 4>(p, s);
+}
 template <int D, bool QF32>
 hipError_t pick(const AttendParams& p, hipStream_t s) {
-    const bool p16 = p.c.page % 16 == 0;
-    if (p.c.kind == KV_BF16) return p16 ? go<D, KV_BF16, QF32, true>(p, s) : go<D, KV_BF16, QF32, false>(p, s);
-    if (p.c.kind == KV_FP8) return p16 ? go<D, KV_FP8, QF32, true>(p, s) : go<D, KV_FP8, QF32, false>(p, s);
-    return p16 ? go<D, KV_FP4, QF32, true>(p, s) : go<D, KV_FP4, QF32, false>(p, s);
+    if (p.c.kind == KV_BF16) return pages<D, KV_BF16, QF32>(p, s);
+    return p.c.kind == KV_FP8 ? pages<D, KV_FP8, QF32>(p, s) : pages<D, KV_FP4, QF32>(p, s);
 }
 
 }  // namespace
@@ -554,17 +685,26 @@ hipError_t launch_cache_write(const CacheWrite& p, bool bf, hipStream_t s) {
 
 bool attend_dim_ok(int d) { return d == 64 || d == 96 || d == 128 || d == 192 || d == 256; }
 
-// Splits: enough workgroups to fill the chip twice over, none shorter than one
-// tile per wave.
-void attend_plan(const KvCache& c, int64_t batch, int q_heads, int64_t cols, int* chunk, int* splits) {
+// How a call is split.  Short sequences (four tiles a wave at most): eight
+// waves take a whole one and no join follows.  Longer ones: workgroups of four
+// waves, as many chunks as fill the chip, none shorter than one tile per wave.
+AttendPlan attend_plan(const KvCache& c, int64_t batch, int q_heads, int64_t cols) {
     const int group = q_heads / c.heads, tiles = (group + QH - 1) / QH;
-    const int64_t units = batch > 0 ? batch * c.heads * tiles : 1, longest = cols * c.page, least = AW * TILE;
-    const int64_t want = 1024;
-    int64_t n = units >= want ? 1 : (want + units - 1) / units;
-    int64_t per = ((longest + n - 1) / n + least - 1) / least * least;
-    if (per < least) per = least;
-    *chunk = (int)per;
-    *splits = longest > 0 ? (int)((longest + per - 1) / per) : 1;
+    const int64_t units = batch > 0 ? batch * c.heads * tiles : 1, longest = cols * c.page;
+    AttendPlan a;
+    if (c.dim <= EIGHT_MAX && (longest <= 8 * TILE || (longest <= 8 * TILE * 4 && units >= 256))) {
+        a.waves = 8;
+        a.chunk = 8 * TILE * 4;
+        a.splits = 1;
+        return a;
+    }
+    a.waves = 4;
+    const int64_t least = 4 * TILE, want = 512;
+    const int64_t n = units >= want ? 1 : (want + units - 1) / units;
+    const int64_t per = ((longest + n - 1) / n + least - 1) / least * least;
+    a.chunk = (int)per;
+    a.splits = (int)((longest + per - 1) / per);
+    return a;
 }
 
 hipError_t launch_attend(AttendParams p, bool bf, hipStream_t s) {

@@ -194,12 +194,16 @@ struct AttendParams {
     float scale;
     float* lse;                    // nullable
     float* parts;                  // splits > 1: [b][q head][split][dim] sums, then [b][q head][split][2] max and sum
-    int chunk, splits;             // tokens per workgroup, workgroups per sequence and head tile
+    int chunk, splits, waves;      // of the plan
     uint32_t page_mul;             // t / page = (t * page_mul) >> page_shift for t < 2^31
     int page_shift;
 };
-// splits and chunk for a cache, batch and table width
-void attend_plan(const KvCache& c, int64_t batch, int q_heads, int64_t cols, int* chunk, int* splits);
+// How a call is split: tokens per workgroup, workgroups per sequence, key-value
+// head and 16 query heads, waves per workgroup
+struct AttendPlan {
+    int chunk, splits, waves;
+};
+AttendPlan attend_plan(const KvCache& c, int64_t batch, int q_heads, int64_t cols);
 bool attend_dim_ok(int dim);
 hipError_t launch_attend(AttendParams p, bool q_bf16, hipStream_t s);
 
