@@ -333,13 +333,13 @@ mxk::KvCache cache_params(const mx_kv_cache* c) {
 int check_attend(const mx_kv_cache* c, int64_t batch, int32_t q_heads, int64_t cols) {
     if (batch < 0 || cols < 0 || q_heads < 1 || q_heads % c->heads) return MX_ERR_ARG;
     if (cols >= ((int64_t)1 << 30) / c->page_size || batch >= (int64_t)1 << 31) return MX_ERR_ARG;
-    if ((double)batch * q_heads * mxk::attend_plan(cache_params(c), batch, q_heads, cols).splits >= 2147483648.0) return MX_ERR_ARG;
+    if ((double)batch * q_heads >= 2147483648.0) return MX_ERR_ARG;
     return MX_OK;
 }
 
 size_t attend_bytes(const mx_kv_cache* c, int64_t batch, int32_t q_heads, int64_t cols) {
-    const int64_t splits = mxk::attend_plan(cache_params(c), batch, q_heads, cols).splits;
-    return splits > 1 ? round_up((size_t)batch * q_heads * splits * (c->dim + 2) * sizeof(float)) : 0;
+    const int64_t workers = mxk::attend_plan(cache_params(c), batch, q_heads, cols).workers;
+    return workers && batch ? round_up((size_t)q_heads * (workers + batch) * (c->dim + 2) * sizeof(float)) : 0;
 }
 
 }  // namespace
@@ -796,9 +796,8 @@ int mx_attend(const mx_kv_cache* cache, const mx_heads* q, int64_t batch, const 
     p.lse = lse;
     p.parts = static_cast<float*>(workspace);
     const mxk::AttendPlan a = mxk::attend_plan(p.c, batch, q->heads, table_cols);
-    p.chunk = a.chunk;
-    p.splits = a.splits;
     p.waves = a.waves;
+    p.workers = a.workers;
     return hip_status(mxk::launch_attend(p, q->dtype == MX_DTYPE_BF16, static_cast<hipStream_t>(stream)));
 }
 

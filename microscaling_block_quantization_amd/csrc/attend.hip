@@ -25,6 +25,10 @@
 //    in registers (one byte permute per two values).
 // FP8 and FP4 values times their block's power of two are exact in bf16 (down
 // to bf16's own smallest values), so a quantized cache costs conversions only.
+// Measured (32 query and 8 key-value heads of 128): 32 sequences up to 8192
+// tokens, bf16, 106 us, 5.3 TB/s of cache (a large copy reaches 5.1); one of
+// 131072, bf16 100 us (5.4), MXFP8 64 us (4.3), MXFP4 47 us (3.0), where the
+// conversions, the softmax and the waits between them no longer hide.
 #include "mx_kernels.hpp"
 
 namespace mxk {
@@ -214,11 +218,104 @@ __device__ __forceinline__ uint32_t pack_hi(uint32_t a, uint32_t b) { return __b
 // Left to itself the scheduler moves loads behind the wait for older ones.
 #define ISSUED __builtin_amdgcn_sched_barrier(0)
 
-// One wave takes every AW-th tile of 32 tokens of the workgroup's chunk.  The
+// How long sequences are shared out.  Lengths are known on the device alone and
+// differ, so the workgroups of a plane ("workers") divide the tokens of all
+// sequences, one after the other in units of 128, into equal ranges: worker w of
+// W takes units [w T / W, (w + 1) T / W) of T (of the first T workers where there
+// are more than units, so that no range is empty).  A range may hold the end of one
+// sequence and the beginning of the next; a sequence within one range is
+// finished there, the others' parts go to slot w + b of their heads (in order, a
+// range's step moves w on and a sequence's step b, so no two share one).
+constexpr int UNIT = 128;
+__device__ __forceinline__ int64_t units_of(int len) { return (len + UNIT - 1) / UNIT; }
+
+__device__ __forceinline__ int workers_used(int64_t units, int workers) { return (int)(units < workers ? units : workers); }
+
+// sum over the workgroup of T threads, in every thread
+template <int T>
+__device__ __forceinline__ int64_t block_total(int64_t v, int64_t* sh) {
+#pragma unroll
+    for (int o = 1; o < 64; o <<= 1) v += __shfl_xor(v, o, 64);
+    if ((threadIdx.x & 63) == 0) sh[threadIdx.x >> 6] = v;
+    __syncthreads();
+    int64_t t = 0;
+#pragma unroll
+    for (int i = 0; i < T / 64; i++) t += sh[i];
+    __syncthreads();
+    return t;
+}
+// Worker w's range, the sequence its first unit lies in and the units before
+// that sequence; false for an empty range.
+template <int T, typename F>
+__device__ __forceinline__ bool share_of(int64_t batch, uint32_t w, int workers, F&& units, int64_t& b, int64_t& before, int64_t& u,
+                                         int64_t& u_end) {
+    __shared__ int64_t sh[T / 64 + 2];
+    const int tid = threadIdx.x, lane = tid & 63;
+    // the same in every thread, and known to be
+    auto uniform = [](int64_t v) {
+        return (int64_t)((uint64_t)(uint32_t)__builtin_amdgcn_readfirstlane((int)(v >> 32)) << 32 |
+                         (uint32_t)__builtin_amdgcn_readfirstlane((int)v));
+    };
+    if (batch <= 64) {                                     // each wave on its own, a sequence a lane (at most 2^29 units)
+        const int n = lane < batch ? (int)units(lane) : 0;
+        int upto = n;
+#pragma unroll
+        for (int o = 1; o < 64; o <<= 1) {
+            const int v = __shfl_up(upto, o, 64);
+            if (lane >= o) upto += v;
+        }
+        const int t = __builtin_amdgcn_readlane(upto, 63), of = workers_used(t, workers);
+        if ((int)w >= of) return false;
+        u = (int64_t)w * t / of;
+        u_end = (int64_t)(w + 1) * t / of;
+        const int at = __ffsll((unsigned long long)__ballot(upto > u)) - 1;      // the first that reaches past unit u
+        b = at;
+        before = __builtin_amdgcn_readlane(upto - n, at);
+        return true;
+    }
+    int64_t mine = 0;
+    for (int64_t i = tid; i < batch; i += T) mine += units(i);
+    const int64_t t = block_total<T>(mine, sh), of = workers_used(t, workers);
+    if (w >= of) return false;
+    u = w * t / of;
+    u_end = (w + 1) * t / of;
+    int64_t run = 0;
+    for (int64_t base = 0;; base += T) {                   // some sequence holds unit u
+        const int64_t n = base + tid < batch ? units(base + tid) : 0;
+        int64_t upto = n;                                  // inclusive sums over the wave
+#pragma unroll
+        for (int o = 1; o < 64; o <<= 1) {
+            const int64_t v = __shfl_up(upto, o, 64);
+            if (lane >= o) upto += v;
+        }
+        if (lane == 63) sh[tid >> 6] = upto;
+        __syncthreads();
+        int64_t lead = run, all = 0;
+#pragma unroll
+        for (int i = 0; i < T / 64; i++) {
+            if (i < (tid >> 6)) lead += sh[i];
+            all += sh[i];
+        }
+        const int64_t from = lead + upto - n;
+        if (from <= u && u < from + n) {
+            sh[T / 64] = base + tid;
+            sh[T / 64 + 1] = from;
+        }
+        __syncthreads();
+        if (u < run + all) break;
+        run += all;
+    }
+    b = uniform(sh[T / 64]);
+    before = uniform(sh[T / 64 + 1]);
+    u = uniform(u);
+    u_end = uniform(u_end);
+    return true;
+}
+
+// One wave takes every AW-th tile of 32 tokens of the workgroup's segment.  The
 // loads of a tile's values go out before its scores are formed, those of the
 // next tile's keys before its second product, so one of the two is always in
-// flight; quantized tiles are small, and all of the next one's loads go out
-// before the scores.  PAGE16: pages of a multiple of 16 tokens, so that 16 tokens share a
+// flight.  PAGE16: pages of a multiple of 16 tokens, so that 16 tokens share a
 // page, whose number is then one scalar load, and reading all 16 stays inside
 // the page whatever the length.
 template <int D, int KIND, bool QF32, bool PAGE16, int AW>
@@ -229,8 +326,6 @@ __global__ __launch_bounds__(64 * AW, D <= 128 ? 2 : 1) void k_attend(AttendPara
     constexpr int KU = count_units(D, unit_max(KIND));     // units of the score product
     constexpr int VU = count_units(D, 128);                // runs of 16 lanes of the second product
     constexpr int LD = D + 1;                              // LDS row of one head's sums
-    // a quantized tile is small enough to hold the next one's keys and values too
-    constexpr bool FAR = KIND != KV_BF16 && PAGE16 && D <= 128 && !QF32;
     // scales of a token (and of the value operand's four tokens) as whole dwords
     constexpr bool WIDE_SC = KIND != KV_BF16 && PAGE16 && (D == 64 || D % 128 == 0);
     extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
@@ -238,23 +333,34 @@ __global__ __launch_bounds__(64 * AW, D <= 128 ? 2 : 1) void k_attend(AttendPara
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int r = lane & 15, g = lane >> 4;
     const int group = p.q_heads / p.c.heads, tiles = (group + QH - 1) / QH;
-    // workgroup -> split (fastest), head tile, key-value head, sequence
-    uint32_t id = blockIdx.x;
-    const int split = (int)(id % (uint32_t)p.splits);
-    id /= (uint32_t)p.splits;
-    const int tile = (int)(id % (uint32_t)tiles);
-    id /= (uint32_t)tiles;
-    const int kvh = (int)(id % (uint32_t)p.c.heads);
-    const int64_t b = id / (uint32_t)p.c.heads;
+    const uint32_t planes = (uint32_t)(p.c.heads * tiles);
+    const int64_t cap = p.cols * p.c.page;
+    auto len_of = [&](int64_t b) {
+        const int64_t n = p.lengths[b];
+        return (int)(n < 0 ? 0 : n > cap ? cap : n);
+    };
+    // This workgroup's plane (key-value head and head tile), first sequence and,
+    // among workers, its share [u, u_end) of the units of all sequences in order;
+    // `before` is the number of units before sequence b.
+    uint32_t plane;
+    int64_t b, u = 0, u_end = 0, before = 0;
+    if (p.workers) {
+        plane = blockIdx.x / (uint32_t)p.workers;
+        const uint32_t w = blockIdx.x - plane * (uint32_t)p.workers;
+        if (!share_of<64 * AW>(p.batch, w, p.workers, [&](int64_t i) { return units_of(len_of(i)); }, b, before, u, u_end)) return;
+    } else {
+        b = blockIdx.x / planes;
+        plane = blockIdx.x - (uint32_t)b * planes;
+    }
+    const int tile = (int)(plane % (uint32_t)tiles), kvh = (int)(plane / (uint32_t)tiles);
     const int h0 = kvh * group + tile * QH;                // first query head
     const int nh = group - tile * QH < QH ? group - tile * QH : QH;
+    const float zs = p.scale * 1.44269504088896340736f;
 
-    const int64_t cap = p.cols * p.c.page;
-    int64_t len64 = p.lengths[b];
-    len64 = len64 < 0 ? 0 : len64 > cap ? cap : len64;
-    const int len = (int)len64, t0 = split * p.chunk;
-    if (t0 >= len && !(len == 0 && split == 0)) return;    // nothing here; the join does not read it
-    const int tend = len < t0 + p.chunk ? len : t0 + p.chunk;
+    while (true) {                                         // a segment of one sequence: tokens [t0, tend)
+    const int len = len_of(b);
+    const int64_t t1 = (u_end - before) * UNIT;
+    const int t0 = p.workers ? (int)((u - before) * UNIT) : 0, tend = p.workers && t1 < len ? (int)t1 : len;
     const int32_t* table = p.table + b * p.table_stride;
 
     bool bad = false;
@@ -373,17 +479,12 @@ __global__ __launch_bounds__(64 * AW, D <= 128 ? 2 : 1) void k_attend(AttendPara
 #pragma unroll
     for (int i = 0; i < D / 16; i++) acc[i] = f4v{0.f, 0.f, 0.f, 0.f};
     float m = -INFINITY, l = 0.f;                          // of head r; l: this lane's tokens
-    const float zs = p.scale * 1.44269504088896340736f;
 
-    // the tile at tb from (keys, val); the next one's loads
-    auto tile_step = [&](int tb, Keys& keys, Values& val, Keys& next_keys, Values& next_val) {
-        if constexpr (!FAR) load_values(val, here);
-        const int next = tb + AW * TILE < tend ? tb + AW * TILE : tb;      // after the last tile: the same again, unused
+    for (int tb = first; tb < tend; tb += AW * TILE) {
+        Values val;
+        load_values(val, here);
+        const int next = tb + AW * TILE < tend ? tb + AW * TILE : tb;      // after the last tile: its keys again, unused
         place(then, next);
-        if constexpr (FAR) {
-            load_keys(next_keys, then);
-            load_values(next_val, then);
-        }
         ISSUED;
 
         // scores
@@ -411,11 +512,9 @@ __global__ __launch_bounds__(64 * AW, D <= 128 ? 2 : 1) void k_attend(AttendPara
                 });
             });
         }
-        if constexpr (!FAR) {
-            ISSUED;
-            load_keys(next_keys, then);
-            ISSUED;
-        }
+        ISSUED;
+        load_keys(keys, then);
+        ISSUED;
 
         // softmax of this lane's 8 tokens of head r
         float zmax = -INFINITY;
@@ -498,21 +597,6 @@ __global__ __launch_bounds__(64 * AW, D <= 128 ? 2 : 1) void k_attend(AttendPara
             });
         });
         here = then;
-    };
-    if constexpr (FAR) {
-        Keys keys2;
-        Values val, val2;
-        if (first < tend) load_values(val, here);
-        for (int tb = first; tb < tend; tb += 2 * AW * TILE) {
-            tile_step(tb, keys, val, keys2, val2);
-            if (tb + AW * TILE >= tend) break;
-            tile_step(tb + AW * TILE, keys2, val2, keys, val);
-        }
-    } else {
-        for (int tb = first; tb < tend; tb += AW * TILE) {
-            Values val;
-            tile_step(tb, keys, val, keys, val);
-        }
     }
 
     // the waves' triples, joined through LDS
@@ -548,26 +632,35 @@ __global__ __launch_bounds__(64 * AW, D <= 128 ? 2 : 1) void k_attend(AttendPara
             o += f * sums[(w * nh + h) * LD + d];
         }
         const int64_t bh = b * p.q_heads + h0 + h;
-        if (p.splits > 1) {
-            p.parts[(bh * p.splits + split) * D + d] = o;
-            if (d == 0) {
-                float* x = p.parts + p.batch * p.q_heads * p.splits * D + (bh * p.splits + split) * 2;
-                x[0] = M;
-                x[1] = L;
-            }
-        } else {
+        if (t0 == 0 && tend == len) {                      // the whole sequence
             const float v = L == 0.f ? 0.f : o / L;
             const int64_t at = b * p.o_ts + (int64_t)(h0 + h) * p.o_hs + d;
             if (QF32) static_cast<float*>(p.o)[at] = v;
             else static_cast<uint16_t*>(p.o)[at] = bf16_rne(v);
             if (p.lse && d == 0) p.lse[bh] = L == 0.f ? -INFINITY : (Ms + log2f(L)) * 0.69314718055994530942f;
+        } else {
+            const int64_t slots = p.workers + p.batch, at = (h0 + h) * slots + (int64_t)(blockIdx.x - plane * (uint32_t)p.workers) + b;
+            p.parts[at * D + d] = o;
+            if (d == 0) {
+                float* x = p.parts + (int64_t)p.q_heads * slots * D + at * 2;
+                x[0] = M;
+                x[1] = L;
+            }
         }
+    }
+    if (!p.workers) break;
+    // the next sequence that holds anything
+    u = before += units_of(len);
+    if (u >= u_end) break;
+    do b++; while (len_of(b) == 0);
+    __syncthreads();                                       // the sums' LDS is used again
     }
 }
 #undef ISSUED
 
-// Joins the splits of one sequence and query head: groups of D / 4 lanes (a
-// power of two of them) take every JG-th split, four values a lane, then their
+// Joins the parts of one sequence and query head, where it has several, and
+// writes the empty ones: groups of D / 4 lanes (a power of two of them) take
+// every JG-th part, four values a lane, then their
 // triples are joined in order.
 template <int D, bool QF32>
 __global__ __launch_bounds__(256) void k_attend_join(AttendParams p) {
@@ -577,12 +670,31 @@ __global__ __launch_bounds__(256) void k_attend_join(AttendParams p) {
     const int64_t bh = blockIdx.x, b = bh / p.q_heads;
     const int h = (int)(bh - b * p.q_heads);
     const int64_t cap = p.cols * p.c.page;
-    int64_t len = p.lengths[b];
-    len = len < 0 ? 0 : len > cap ? cap : len;
-    int used = (int)((len + p.chunk - 1) / p.chunk);
-    if (used < 1) used = 1;                          // an empty sequence's first workgroup leaves sum 0
-    const float* o = p.parts + bh * p.splits * D + (4 * u < D ? 4 * u : 0);
-    const float* x = p.parts + p.batch * p.q_heads * p.splits * D + bh * p.splits * 2;
+    auto units = [&](int64_t i) {
+        const int64_t n = p.lengths[i];
+        return units_of((int)(n < 0 ? 0 : n > cap ? cap : n));
+    };
+    const int64_t n = units(b);
+    int64_t t = n, before = 0;
+    if (p.batch > 1) {
+        __shared__ int64_t sh[256 / 64];
+        int64_t mine = 0, less = 0;
+        for (int64_t i = threadIdx.x; i < p.batch; i += 256) {
+            const int64_t v = units(i);
+            mine += v;
+            if (i < b) less += v;
+        }
+        t = block_total<256>(mine, sh);
+        before = block_total<256>(less, sh);
+    }
+    // the workers that hold its first and last unit
+    const int64_t of = workers_used(t, p.workers);
+    const int64_t from = n ? ((before + 1) * of - 1) / t : 0, to = n ? ((before + n) * of - 1) / t : 0;
+    if (n && from == to) return;                     // finished there
+    const int used = n ? (int)(to - from + 1) : 0;
+    const int64_t slots = p.workers + p.batch, at0 = h * slots + from + b;
+    const float* o = p.parts + at0 * D + (4 * u < D ? 4 * u : 0);
+    const float* x = p.parts + (int64_t)p.q_heads * slots * D + at0 * 2;
     float M = -INFINITY, L = 0.f;
     f4v v = {0.f, 0.f, 0.f, 0.f};
     for (int i = grp; i < used; i += JG * AHEAD) {
@@ -639,7 +751,7 @@ __global__ __launch_bounds__(256) void k_attend_join(AttendParams p) {
 template <int D, int KIND, bool QF32, bool PAGE16, int AW>
 hipError_t go(const AttendParams& p, hipStream_t s) {
     const int group = p.q_heads / p.c.heads, tiles = (group + QH - 1) / QH, rows = group < QH ? group : QH;
-    const int64_t n = p.batch * p.c.heads * tiles * p.splits;
+    const int64_t n = p.c.heads * tiles * (p.workers ? p.workers : p.batch);
     const int lds = AW * rows * (D + 3) * (int)sizeof(float);
     if (lds > 64 * 1024) {
         const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(k_attend<D, KIND, QF32, PAGE16, AW>),
@@ -648,7 +760,7 @@ hipError_t go(const AttendParams& p, hipStream_t s) {
     }
     k_attend<D, KIND, QF32, PAGE16, AW><<<(unsigned)n, 64 * AW, lds, s>>>(p);
     hipError_t e = hipGetLastError();
-    if (e != hipSuccess || p.splits == 1) return e;
+    if (e != hipSuccess || !p.workers) return e;
     k_attend_join<D, QF32><<<(unsigned)(p.batch * p.q_heads), 256, 0, s>>>(p);
     return hipGetLastError();
 }
@@ -685,26 +797,23 @@ hipError_t launch_cache_write(const CacheWrite& p, bool bf, hipStream_t s) {
 
 bool attend_dim_ok(int d) { return d == 64 || d == 96 || d == 128 || d == 192 || d == 256; }
 
-// How a call is split.  Short sequences (four tiles a wave at most): eight
-// waves take a whole one and no join follows.  Longer ones: workgroups of four
-// waves, as many chunks as fill the chip, none shorter than one tile per wave.
+// How a call is split.  Short sequences (one tile a wave, or four if there are
+// enough of them to fill the chip): eight waves take a whole one and no join
+// follows (32 sequences of 777: 17 us, shared out 25; one of 777: 12 us, shared
+// out 9.8).  Others: workers, one workgroup of four waves for each CU where a
+// token's row is 256 bytes or more, so that four waves keep enough in flight,
+// three where it is less (us with 256 workgroups and with 768, 32 sequences up
+// to 8192 tokens of 128 values: bf16 106 and 120, MXFP8 84 and 68, MXFP4 71 and
+// 52; bf16 of 64 values, half the tokens: 44 and 37).
 AttendPlan attend_plan(const KvCache& c, int64_t batch, int q_heads, int64_t cols) {
-    const int group = q_heads / c.heads, tiles = (group + QH - 1) / QH;
-    const int64_t units = batch > 0 ? batch * c.heads * tiles : 1, longest = cols * c.page;
-    AttendPlan a;
-    if (c.dim <= EIGHT_MAX && (longest <= 8 * TILE || (longest <= 8 * TILE * 4 && units >= 256))) {
-        a.waves = 8;
-        a.chunk = 8 * TILE * 4;
-        a.splits = 1;
-        return a;
-    }
-    a.waves = 4;
-    const int64_t least = 4 * TILE, want = 512;
-    const int64_t n = units >= want ? 1 : (want + units - 1) / units;
-    const int64_t per = ((longest + n - 1) / n + least - 1) / least * least;
-    a.chunk = (int)per;
-    a.splits = (int)((longest + per - 1) / per);
-    return a;
+    const int group = q_heads / c.heads;
+    const int64_t planes = (int64_t)c.heads * ((group + QH - 1) / QH), longest = cols * c.page;
+    if (c.dim <= EIGHT_MAX && (longest <= 8 * TILE || (longest <= 8 * TILE * 4 && batch * planes >= 256))) return AttendPlan{8, 0};
+    const int64_t want = c.dim * kind_bits(c.kind) / 8 >= 256 ? 256 : 768;
+    int64_t workers = (want + planes - 1) / planes;
+    const int64_t most = batch * ((longest + UNIT - 1) / UNIT);
+    if (workers > most) workers = most;
+    return AttendPlan{4, (int)(workers < 1 ? 1 : workers)};
 }
 
 hipError_t launch_attend(AttendParams p, bool bf, hipStream_t s) {

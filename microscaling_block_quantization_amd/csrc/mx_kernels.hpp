@@ -193,15 +193,15 @@ struct AttendParams {
     const int32_t* lengths;
     float scale;
     float* lse;                    // nullable
-    float* parts;                  // splits > 1: [b][q head][split][dim] sums, then [b][q head][split][2] max and sum
-    int chunk, splits, waves;      // of the plan
+    float* parts;                  // with workers: [q head][worker + sequence][dim] sums, then [..][2] max and sum
+    int waves, workers;            // of the plan
     uint32_t page_mul;             // t / page = (t * page_mul) >> page_shift for t < 2^31
     int page_shift;
 };
-// How a call is split: tokens per workgroup, workgroups per sequence, key-value
-// head and 16 query heads, waves per workgroup
+// How a call is split: waves per workgroup; 0, or the workgroups that share the
+// tokens of all sequences for each key-value head and 16 query heads
 struct AttendPlan {
-    int chunk, splits, waves;
+    int waves, workers;
 };
 AttendPlan attend_plan(const KvCache& c, int64_t batch, int q_heads, int64_t cols);
 bool attend_dim_ok(int dim);

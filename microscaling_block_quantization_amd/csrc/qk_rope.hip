@@ -110,13 +110,14 @@ __device__ __forceinline__ void turn(float* v, const float* c, const float* s, b
 // the table gives NaN
 __device__ __forceinline__ void load_turn(const RopeParams& p, int64_t token, int i0, float* c, float* s) {
     const int pos = p.positions[token];
-    if (pos >= 0 && (int64_t)pos < p.table_rows) {
-        const int64_t at = (int64_t)pos * (p.rot / 2) + i0;
-        load8<false>(c, p.cos, at);
-        load8<false>(s, p.sin, at);
-    } else {
+    const bool ok = pos >= 0 && (int64_t)pos < p.table_rows;
+    const int64_t at = (int64_t)(ok ? pos : 0) * (p.rot / 2) + i0;
+    load8<false>(c, p.cos, at);
+    load8<false>(s, p.sin, at);
 #pragma unroll
-        for (int i = 0; i < 8; i++) c[i] = s[i] = bitsf(0x7fc00000u);
+    for (int i = 0; i < 8; i++) {
+        c[i] = ok ? c[i] : bitsf(0x7fc00000u);
+        s[i] = ok ? s[i] : bitsf(0x7fc00000u);
     }
 }
 
