@@ -419,16 +419,16 @@ def _raw(t):
 
 def _heads(t, dim, dev, what):
     """The mx_heads of a tokens x heads x dim tensor whose last dimension is contiguous."""
-    st = t.stride()
-    if len(st) != 3 or t.size(2) != dim or st[2] != 1 or t.get_device() != dev:
+    sh, st = t.shape, t.stride()
+    if len(sh) != 3 or sh[2] != dim or st[2] != 1 or t.get_device() != dev:
         raise ValueError(f"{what}: expected tokens x heads x {dim} on one device, the last dimension contiguous")
-    return _PACK_HEADS(t.data_ptr(), st[0], st[1], t.size(1), _code(t.dtype))
+    return _PACK_HEADS(t.data_ptr(), st[0], st[1], sh[1], _code(t.dtype))
 
 
-def _vector(t, n, dtype, dev, what):
-    """Checks n contiguous values (of dtype, unless None)."""
-    if t.dim() != 1 or t.size(0) != n or not t.is_contiguous() or t.get_device() != dev or (dtype is not None and t.dtype != dtype):
-        raise ValueError(f"{what}: expected {n} contiguous values{'' if dtype is None else f' of {dtype}'} on the inputs' device")
+def _vector(t, n, dtype, dev, where, name):
+    """The address of n contiguous values (of dtype, unless None)."""
+    if t.shape != (n,) or not t.is_contiguous() or t.get_device() != dev or (dtype is not None and t.dtype != dtype):
+        raise ValueError(f"{where}: {name} must be {n} contiguous values{'' if dtype is None else f' of {dtype}'} on the inputs' device")
     return t.data_ptr()
 
 
@@ -444,7 +444,7 @@ def mx_matvec(fmt: Format, w: QTensor, x: torch.Tensor, bias=None, y=None, out_d
     ldx, last = x.stride()
     if last != 1 and k > 1 and tokens:
         raise ValueError("mx_matvec: the rows of x must be contiguous")
-    bp = 0 if bias is None else _vector(bias, n, x.dtype, dev, "mx_matvec: bias")
+    bp = 0 if bias is None else _vector(bias, n, x.dtype, dev, "mx_matvec", "bias")
     if y is None:
         y = x.new_empty((tokens, n)) if out_dtype is None else x.new_empty((tokens, n), dtype=out_dtype)
         ldy = n
@@ -466,19 +466,19 @@ def _rope_args(q, k, cos, sin, positions, q_weight, k_weight, eps, interleaved, 
     """The mx_rope of a call, its shapes checked."""
     tokens, _, dim = q.shape
     dev = q.get_device()
+    if (cos.dim() != 2 or cos.shape != sin.shape or cos.dtype != torch.float32 or sin.dtype != torch.float32 or
+            not cos.is_contiguous() or not sin.is_contiguous() or cos.get_device() != dev or sin.get_device() != dev):
+        raise ValueError(f"{where}: cos and sin must be contiguous fp32 tables of positions x rot_dim/2")
     rows, half = cos.shape
-    for t in (cos, sin):
-        if t.dtype != torch.float32 or not t.is_contiguous() or t.get_device() != dev or t.size(0) != rows or t.size(1) != half:
-            raise ValueError(f"{where}: cos and sin must be contiguous fp32 tables of positions x rot_dim/2")
-    pos = _vector(positions, tokens, torch.int32, dev, where + ": positions")
+    pos = _vector(positions, tokens, torch.int32, dev, where, "positions")
     wd = DTYPE_F32
     qp = kp = 0
     if q_weight is not None:
-        qp, wd = _vector(q_weight, dim, None, dev, where + ": q_weight"), _code(q_weight.dtype)
+        qp, wd = _vector(q_weight, dim, None, dev, where, "q_weight"), _code(q_weight.dtype)
     if k_weight is not None:
         if k is None or (q_weight is not None and q_weight.dtype != k_weight.dtype):
             raise ValueError(f"{where}: k_weight needs k, and the dtype of q_weight")
-        kp, wd = _vector(k_weight, dim, None, dev, where + ": k_weight"), _code(k_weight.dtype)
+        kp, wd = _vector(k_weight, dim, None, dev, where, "k_weight"), _code(k_weight.dtype)
     if k is not None and k.size(0) != tokens:
         raise ValueError(f"{where}: q and k differ in tokens")
     return _PACK_ROPE(tokens, dim, 2 * half, 1 if interleaved else 0, wd, qp, kp, cos.data_ptr(), sin.data_ptr(), rows, pos, eps)
@@ -488,7 +488,9 @@ def _out_heads(out, like, dim, dev, what):
     """An output of `like`'s shape (a new tensor when None) and its mx_heads."""
     if out is None:
         out = torch.empty_like(like, memory_format=torch.contiguous_format)
-    elif out.shape != like.shape:
+        n = like.size(1)
+        return out, _PACK_HEADS(out.data_ptr(), n * dim, dim, n, _DTYPES[like.dtype])
+    if out.shape != like.shape:
         raise ValueError(f"{what}: expected the shape {tuple(like.shape)}")
     return out, _heads(out, dim, dev, what)
 
@@ -543,7 +545,7 @@ def mx_qk_rope_backward(dy_q, dy_k, q, k, cos, sin, positions, q_weight=None, k_
     dqw = None if q_weight is None else cos.new_empty((dim,))
     dkw = None if k_weight is None else cos.new_empty((dim,))
     if workspace is None and (dqw is not None or dkw is not None):
-        workspace = _empty(lib().mx_qk_rope_workspace_size(r), q.device)
+        workspace = cos.new_empty((lib().mx_qk_rope_workspace_size(r),), dtype=torch.uint8)
     _check(lib().mx_qk_rope_backward(r, gq, gk, xq, xk, oq, ok, _raw(dqw), _raw(dkw), _raw(workspace),
                                      0 if workspace is None else workspace.numel(), _stream_ptr(stream)), "mx_qk_rope_backward")
     return dq, dk, dqw, dkw
@@ -611,7 +613,7 @@ def mx_cache_write(cache: KVCache, k, v, slots, stream=None):
     tokens = k.size(0)
     if v.size(0) != tokens:
         raise ValueError("mx_cache_write: k and v differ in tokens")
-    at = _vector(slots, tokens, torch.int64, dev, "mx_cache_write: slots")
+    at = _vector(slots, tokens, torch.int64, dev, "mx_cache_write", "slots")
     _check(lib().mx_cache_write(cache._ref, hk, hv, tokens, at, _stream_ptr(stream)), "mx_cache_write")
     return cache
 
@@ -641,15 +643,15 @@ def mx_attend(q, cache: KVCache, page_table, lengths, scale=None, out=None, lse=
     stride, last = page_table.stride()
     if last != 1 and cols > 1 and batch:
         raise ValueError("mx_attend: the rows of page_table must be contiguous")
-    n = _vector(lengths, batch, torch.int32, dev, "mx_attend: lengths")
+    n = _vector(lengths, batch, torch.int32, dev, "mx_attend", "lengths")
     out, ho = _out_heads(out, q, dim, dev, "mx_attend: out")
     if lse is True:
-        lse = torch.empty((batch, heads), dtype=torch.float32, device=q.device)
+        lse = q.new_empty((batch, heads), dtype=torch.float32)
     elif lse is not None and (lse.shape != (batch, heads) or lse.dtype != torch.float32 or not lse.is_contiguous() or
                               lse.get_device() != dev):
         raise ValueError(f"mx_attend: lse must be a contiguous fp32 {batch} x {heads}")
     if workspace is None:
-        workspace = _empty(lib().mx_attend_workspace_size(cache._ref, batch, heads, cols), q.device)
+        workspace = cache.k.new_empty((lib().mx_attend_workspace_size(cache._ref, batch, heads, cols),), dtype=torch.uint8)
     _check(lib().mx_attend(cache._ref, hq, batch, page_table.data_ptr(), cols, cols if batch <= 1 else stride, n,
                            dim ** -0.5 if scale is None else scale, ho, _raw(lse), workspace.data_ptr(), workspace.numel(),
                            _stream_ptr(stream)), "mx_attend")

@@ -8,6 +8,7 @@
 #include <atomic>
 
 #include "../../include/mx.h"
+#include "decode_kernels.hpp"
 #include "mx_kernels.hpp"
 
 using mxk::QParams;

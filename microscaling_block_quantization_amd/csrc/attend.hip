@@ -29,7 +29,7 @@
 // tokens, bf16, 106 us, 5.3 TB/s of cache (a large copy reaches 5.1); one of
 // 131072, bf16 100 us (5.4), MXFP8 64 us (4.3), MXFP4 47 us (3.0), where the
 // conversions, the softmax and the waits between them no longer hide.
-#include "mx_kernels.hpp"
+#include "decode_kernels.hpp"
 
 namespace mxk {
 using namespace mxd;

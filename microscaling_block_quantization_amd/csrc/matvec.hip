@@ -40,7 +40,7 @@
 // per step 52 to 83, sixteen waves 42, codes two tiles ahead 42.
 #include <type_traits>
 
-#include "mx_kernels.hpp"
+#include "decode_kernels.hpp"
 
 namespace mxk {
 using namespace mxd;

@@ -120,91 +120,4 @@ hipError_t launch_gemm_upcvt(int sca, int bca, const uint8_t* a, const uint8_t* 
                              int64_t K, int64_t ldc, int c_bf16, hipStream_t s, const uint8_t* ma = nullptr,
                              const uint8_t* mb = nullptr);
 
-// ---- the decode step (matvec.hip, qk_rope.hip, attend.hip) --------------------
-struct MatvecParams {
-    const uint8_t* codes;          // n x k/2
-    const uint8_t* scales;         // n x k / block
-    const uint16_t* offsets;       // nullable: bf16, n x k / block
-    const uint8_t* macro;          // nullable: UE4M3, n x k/128
-    const float* tensor_scale;     // nullable
-    int64_t n, k;
-    int elem, scale, lgb;          // lgb: log2 of the block width
-    const void* x;                 // tokens x k, row stride ldx
-    int64_t tokens, ldx;
-    int x_bf16;
-    const void* bias;              // nullable, the dtype of x
-    void* y;
-    int64_t ldy;
-    int y_bf16;
-};
-hipError_t launch_matvec(const MatvecParams& p, hipStream_t s);
-
-// queries or keys of a norm-and-rotation launch; strides in elements
-struct RopeSet {
-    const void* x;                 // the input heads
-    const void* g;                 // backward: the outputs' gradient
-    void* y;                       // the output heads, or the inputs' gradient
-    int64_t x_ts, x_hs, g_ts, g_hs, y_ts, y_hs;
-    uint32_t heads;                // 0: no such set
-    const void* w;                 // nullable
-    float* dw;                     // backward, where w is set
-    float* parts;                  // backward: partial sums of dw, one row per workgroup
-    uint32_t b0, nb;               // set by the launcher: this set's workgroups
-};
-struct RopeParams {
-    RopeSet set[2];
-    int64_t tokens, table_rows;
-    int dim, rot, adjacent, w_bf16;
-    const float *cos, *sin;
-    const int32_t* positions;
-    float eps;
-};
-constexpr int ROPE_PARTS = 1024;   // most workgroups (and partial rows) per set of a backward launch
-hipError_t launch_rope(RopeParams p, bool bf16, bool back, hipStream_t s);
-
-// cache element kinds
-enum { KV_BF16 = 0, KV_FP8 = 1, KV_FP4 = 2 };
-struct KvCache {
-    uint8_t *k, *v, *ks, *vs;      // ks, vs: E8M0 scales, null for KV_BF16
-    int64_t pages;
-    int page, heads, dim, kind;
-};
-struct CacheWrite {
-    KvCache c;
-    const void *k, *v;
-    int64_t k_ts, k_hs, v_ts, v_hs;
-    const int64_t* slots;
-    int64_t tokens;
-    int rule;                      // E8M0 exponent rule
-    float tau;
-};
-hipError_t launch_cache_write(const CacheWrite& p, bool in_bf16, hipStream_t s);
-
-struct AttendParams {
-    KvCache c;
-    const void* q;
-    int64_t q_ts, q_hs;
-    void* o;
-    int64_t o_ts, o_hs;
-    int64_t batch;
-    int q_heads;
-    const int32_t* table;
-    int64_t cols, table_stride;
-    const int32_t* lengths;
-    float scale;
-    float* lse;                    // nullable
-    float* parts;                  // with workers: [q head][worker + sequence][dim] sums, then [..][2] max and sum
-    int waves, workers;            // of the plan
-    uint32_t page_mul;             // t / page = (t * page_mul) >> page_shift for t < 2^31
-    int page_shift;
-};
-// How a call is split: waves per workgroup; 0, or the workgroups that share the
-// tokens of all sequences for each key-value head and 16 query heads
-struct AttendPlan {
-    int waves, workers;
-};
-AttendPlan attend_plan(const KvCache& c, int64_t batch, int q_heads, int64_t cols);
-bool attend_dim_ok(int dim);
-hipError_t launch_attend(AttendParams p, bool q_bf16, hipStream_t s);
-
 }  // namespace mxk

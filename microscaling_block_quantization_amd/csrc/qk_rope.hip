@@ -19,7 +19,7 @@
 // Measured (8192 tokens of 32 + 8 heads of 128, bf16, back to back): forward
 // 37 us, 4.6 TB/s; backward with its weight sums 60 us, 4.3 TB/s; a large copy
 // reaches 5.1.
-#include "mx_kernels.hpp"
+#include "decode_kernels.hpp"
 
 // nothing here is held to bits: fused multiply-adds are as exact and half the work
 #pragma clang fp contract(fast)
