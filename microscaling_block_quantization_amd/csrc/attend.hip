@@ -66,39 +66,56 @@ __device__ __forceinline__ bf8v frag(uint32_t a, uint32_t b, uint32_t c, uint32_
 // ---------------------------------------------------------------------------
 constexpr int CT = 256;
 
-template <int KIND, bool BF>
+// t / d for t < 2^31 by a multiply: mul = ceil(2^shift / d), 2^shift >= 2^31 d
+__device__ __forceinline__ uint32_t over(uint32_t t, Div d) { return (uint32_t)(((uint64_t)t * d.mul) >> d.shift); }
+Div div_by(int d) {
+    int lg = 0;
+    while ((1 << lg) < d) lg++;
+    Div o;
+    o.shift = 31 + lg;
+    o.mul = (uint32_t)((((uint64_t)1 << o.shift) + d - 1) / d);
+    return o;
+}
+
+// D: the head dimension, known here because a division by a number that is not
+// costs more than everything else a lane does.  A lane takes the key and the
+// value of its place, both loads at once.
+template <int D, int KIND, bool BF>
 __global__ __launch_bounds__(CT) void k_cache_write(CacheWrite p) {
-    const uint32_t units = p.c.dim / 8;
-    const uint64_t i = (uint64_t)blockIdx.x * CT + threadIdx.x;
-    const uint32_t item = (uint32_t)(i / units), u = (uint32_t)(i - (uint64_t)item * units);
-    const uint32_t token = item / (2 * p.c.heads), hv = item - token * (2 * p.c.heads);
-    if ((int64_t)token >= p.tokens) return;              // whole blocks of four lanes leave
-    const bool isv = hv >= (uint32_t)p.c.heads;
-    const int head = isv ? hv - p.c.heads : hv;
+    constexpr uint32_t UNITS = D / 8, PER = CT / UNITS;           // lanes of a vector, vectors of a workgroup
+    const uint32_t n = threadIdx.x / UNITS, u = threadIdx.x - n * UNITS;
+    const uint32_t item = blockIdx.x * PER + n;                   // (token, head)
+    const uint32_t token = over(item, p.per_token), head = item - token * p.c.heads;
+    if (n >= PER || (int64_t)token >= p.tokens) return;           // whole blocks of four lanes leave
+    u32x4 raw[2][BF ? 1 : 2];
+#pragma unroll
+    for (int v = 0; v < 2; v++) {
+        const int64_t src = (int64_t)token * (v ? p.v_ts : p.k_ts) + (int64_t)head * (v ? p.v_hs : p.k_hs) + 8 * u;
+        const u32x4* in = BF ? reinterpret_cast<const u32x4*>(static_cast<const uint16_t*>(v ? p.v : p.k) + src)
+                             : reinterpret_cast<const u32x4*>(static_cast<const float*>(v ? p.v : p.k) + src);
+#pragma unroll
+        for (int i = 0; i < (BF ? 1 : 2); i++) raw[v][i] = in[i];
+    }
     const int64_t slot = p.slots[token];
     if (slot < 0 || slot >= p.c.pages * p.c.page) return;
-    const int64_t src = (int64_t)token * (isv ? p.v_ts : p.k_ts) + (int64_t)head * (isv ? p.v_hs : p.k_hs) + 8 * u;
-    const int64_t page = slot / p.c.page, row = (page * p.c.heads + head) * p.c.page + (slot - page * p.c.page);
-    uint8_t* dst = (isv ? p.c.v : p.c.k);
-    const void* in = isv ? p.v : p.k;
-    float x[8];
-    u32x4 raw = {0u, 0u, 0u, 0u};
-    if constexpr (BF) {
-        raw = *reinterpret_cast<const u32x4*>(static_cast<const uint16_t*>(in) + src);
+    const int64_t page = p.page_shift >= 0 ? slot >> p.page_shift : slot < (1ll << 31) ? over((uint32_t)slot, p.page_div) : slot / p.c.page;
+    const int64_t row = (page * p.c.heads + head) * p.c.page + (slot - page * p.c.page);
 #pragma unroll
-        for (int e = 0; e < 4; e++) { x[2 * e] = bf16lo(raw[e]); x[2 * e + 1] = bf16hi(raw[e]); }
-    } else {
-        const float4* s = reinterpret_cast<const float4*>(static_cast<const float*>(in) + src);
-        const float4 a = s[0], b = s[1];
-        x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w; x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
-    }
-    if constexpr (KIND == KV_BF16) {
-        if constexpr (!BF) {
+    for (int v = 0; v < 2; v++) {
+        uint8_t* dst = v ? p.c.v : p.c.k;
+        float x[8];
 #pragma unroll
-            for (int e = 0; e < 4; e++) raw[e] = (uint32_t)bf16_rne(x[2 * e]) | (uint32_t)bf16_rne(x[2 * e + 1]) << 16;
+        for (int e = 0; e < 8; e++)
+            x[e] = BF ? ((e & 1) ? bf16hi(raw[v][0][e / 2]) : bf16lo(raw[v][0][e / 2])) : bitsf(raw[v][BF ? 0 : e / 4][e % 4]);
+        if constexpr (KIND == KV_BF16) {
+            u32x4 o = raw[v][0];
+            if constexpr (!BF) {
+#pragma unroll
+                for (int e = 0; e < 4; e++) o[e] = (uint32_t)bf16_rne(x[2 * e]) | (uint32_t)bf16_rne(x[2 * e + 1]) << 16;
+            }
+            *reinterpret_cast<u32x4*>(dst + (row * D + 8 * u) * 2) = o;
+            continue;
         }
-        *reinterpret_cast<u32x4*>(dst + (row * p.c.dim + 8 * u) * 2) = raw;
-    } else {
         uint32_t am = 0;
 #pragma unroll
         for (int e = 0; e < 8; e++) am = max(am, fbits(x[e]) & 0x7fffffffu);
@@ -108,7 +125,6 @@ __global__ __launch_bounds__(CT) void k_cache_write(CacheWrite p) {
         const Elem E = make_elem(KIND == KV_FP8 ? E4M3 : E2M1, 0);
         const uint32_t code = bad ? 255u : (uint32_t)(e8m0_exp(p.rule, p.tau, E, bitsf(am)) + 127);
         const float scale = bitsf(code << 23);
-        uint8_t* sc = (isv ? p.c.vs : p.c.ks) + row * (p.c.dim / 32) + u / 4;
         if constexpr (KIND == KV_FP8) {
             // 448 2^e; past the fp32 range no value exceeds it
             const float c = bitsf(code + 8 >= 255 ? 0x7f800000u : ((code + 8) << 23) | 0x600000u);
@@ -122,16 +138,16 @@ __global__ __launch_bounds__(CT) void k_cache_write(CacheWrite p) {
                                                              __builtin_amdgcn_fmed3f(x[4 * h + 3], -c, c), scale, true);
                 __builtin_memcpy(&w[h], &r, 4);
             }
-            *reinterpret_cast<uint2*>(dst + row * p.c.dim + 8 * u) = make_uint2(bad ? 0u : w[0], bad ? 0u : w[1]);
+            *reinterpret_cast<uint2*>(dst + row * D + 8 * u) = make_uint2(bad ? 0u : w[0], bad ? 0u : w[1]);
         } else {
             uint32_t w = 0;
             w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, x[0], x[1], scale, 0);
             w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, x[2], x[3], scale, 1);
             w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, x[4], x[5], scale, 2);
             w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, x[6], x[7], scale, 3);
-            *reinterpret_cast<uint32_t*>(dst + row * (p.c.dim / 2) + 4 * u) = bad ? 0u : w;
+            *reinterpret_cast<uint32_t*>(dst + row * (D / 2) + 4 * u) = bad ? 0u : w;
         }
-        if (u % 4 == 0) *sc = (uint8_t)code;
+        if (u % 4 == 0) (v ? p.c.vs : p.c.ks)[row * (D / 32) + u / 4] = (uint8_t)code;
     }
 }
 
@@ -366,7 +382,7 @@ __global__ __launch_bounds__(64 * AW, D <= 128 ? 2 : 1) void k_attend(AttendPara
     bool bad = false;
     // cache row of token t (page lookup); a bad page reads page 0
     auto row_of = [&](int t) -> int64_t {
-        const uint32_t pg = (uint32_t)(((uint64_t)(uint32_t)t * p.page_mul) >> p.page_shift);
+        const uint32_t pg = over((uint32_t)t, p.page_div);
         int64_t n = table[pg];
         if (n < 0 || n >= p.c.pages) { n = 0; bad = true; }
         return (n * p.c.heads + kvh) * p.c.page + (t - (int)pg * p.c.page);
@@ -777,22 +793,35 @@ hipError_t pick(const AttendParams& p, hipStream_t s) {
     return p.c.kind == KV_FP8 ? pages<D, KV_FP8, QF32>(p, s) : pages<D, KV_FP4, QF32>(p, s);
 }
 
+template <int D, int KIND>
+hipError_t write_as(const CacheWrite& p, bool bf, hipStream_t s) {
+    constexpr int PER = CT / (D / 8);
+    const int64_t n = p.tokens * p.c.heads;
+    const unsigned grid = (unsigned)((n + PER - 1) / PER);
+    if (bf) k_cache_write<D, KIND, true><<<grid, CT, 0, s>>>(p);
+    else k_cache_write<D, KIND, false><<<grid, CT, 0, s>>>(p);
+    return hipGetLastError();
+}
+template <int D>
+hipError_t write_dim(const CacheWrite& p, bool bf, hipStream_t s) {
+    if (p.c.kind == KV_BF16) return write_as<D, KV_BF16>(p, bf, s);
+    return p.c.kind == KV_FP8 ? write_as<D, KV_FP8>(p, bf, s) : write_as<D, KV_FP4>(p, bf, s);
+}
+
 }  // namespace
 
-hipError_t launch_cache_write(const CacheWrite& p, bool bf, hipStream_t s) {
-    const int64_t n = p.tokens * 2 * p.c.heads * (p.c.dim / 8);
-    const unsigned grid = (unsigned)((n + CT - 1) / CT);
-    if (p.c.kind == KV_BF16) {
-        if (bf) k_cache_write<KV_BF16, true><<<grid, CT, 0, s>>>(p);
-        else k_cache_write<KV_BF16, false><<<grid, CT, 0, s>>>(p);
-    } else if (p.c.kind == KV_FP8) {
-        if (bf) k_cache_write<KV_FP8, true><<<grid, CT, 0, s>>>(p);
-        else k_cache_write<KV_FP8, false><<<grid, CT, 0, s>>>(p);
-    } else {
-        if (bf) k_cache_write<KV_FP4, true><<<grid, CT, 0, s>>>(p);
-        else k_cache_write<KV_FP4, false><<<grid, CT, 0, s>>>(p);
+hipError_t launch_cache_write(CacheWrite p, bool bf, hipStream_t s) {
+    p.per_token = div_by(p.c.heads);
+    p.page_div = div_by(p.c.page);
+    p.page_shift = -1;
+    if ((p.c.page & (p.c.page - 1)) == 0) p.page_shift = __builtin_ctz((unsigned)p.c.page);
+    switch (p.c.dim) {
+    case 64: return write_dim<64>(p, bf, s);
+    case 96: return write_dim<96>(p, bf, s);
+    case 128: return write_dim<128>(p, bf, s);
+    case 192: return write_dim<192>(p, bf, s);
+    default: return write_dim<256>(p, bf, s);
     }
-    return hipGetLastError();
 }
 
 bool attend_dim_ok(int d) { return d == 64 || d == 96 || d == 128 || d == 192 || d == 256; }
@@ -817,12 +846,7 @@ AttendPlan attend_plan(const KvCache& c, int64_t batch, int q_heads, int64_t col
 }
 
 hipError_t launch_attend(AttendParams p, bool bf, hipStream_t s) {
-    // t / page by a multiply: mul = ceil(2^sh / page) with 2^sh >= 2^31 page,
-    // exact for t < 2^31; mul < 2^32
-    int lg = 0;
-    while ((1 << lg) < p.c.page) lg++;
-    p.page_shift = 31 + lg;
-    p.page_mul = (uint32_t)((((uint64_t)1 << p.page_shift) + p.c.page - 1) / p.c.page);
+    p.page_div = div_by(p.c.page);
     switch (p.c.dim) {
     case 64: return bf ? pick<64, false>(p, s) : pick<64, true>(p, s);
     case 96: return bf ? pick<96, false>(p, s) : pick<96, true>(p, s);

@@ -55,6 +55,11 @@ struct KvCache {
     int64_t pages;
     int page, heads, dim, kind;
 };
+// a division of numbers below 2^31 as a multiply and a shift
+struct Div {
+    uint32_t mul;
+    int shift;
+};
 struct CacheWrite {
     KvCache c;
     const void *k, *v;
@@ -63,8 +68,10 @@ struct CacheWrite {
     int64_t tokens;
     int rule;                      // E8M0 exponent rule
     float tau;
+    Div per_token, page_div;       // set by the launcher: by the heads, by the page size
+    int page_shift;                // its logarithm where it is a power of two, else -1
 };
-hipError_t launch_cache_write(const CacheWrite& p, bool in_bf16, hipStream_t s);
+hipError_t launch_cache_write(CacheWrite p, bool in_bf16, hipStream_t s);
 
 struct AttendParams {
     KvCache c;
@@ -81,8 +88,7 @@ struct AttendParams {
     float* lse;                    // nullable
     float* parts;                  // with workers: [q head][worker + sequence][dim] sums, then [..][2] max and sum
     int waves, workers;            // of the plan
-    uint32_t page_mul;             // t / page = (t * page_mul) >> page_shift for t < 2^31
-    int page_shift;
+    Div page_div;                  // set by the launcher
 };
 // How a call is split: waves per workgroup; 0, or the workgroups that share the
 // tokens of all sequences for each key-value head and 16 query heads
