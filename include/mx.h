@@ -301,7 +301,9 @@ int mx_gemm(const mx_format *fa, const mx_qtensor *a, const mx_format *fb,
  * in this library's formats: the product of a few unquantized tokens with a
  * 4-bit weight, the norm and rotation of query and key heads (with its
  * gradient, for training), the write of new keys and values to a paged cache,
- * and the attention of one new token per sequence over that cache.           */
+ * and the attention of one new token per sequence over that cache.  Index
+ * vectors (positions, slots, lengths, page numbers) and lse need the alignment
+ * of their elements alone, so slices of them serve.                          */
 
 /* y = x . deq(W)^T + bias for a few tokens: x is tokens x w->cols (row stride
  * ldx elements, dtype x_dtype), W a quantized tensor of w->rows x w->cols, y

@@ -252,6 +252,8 @@ int static_scratch(uint8_t** ptr) {
 }
 
 // ---- checks of the decode-step entry points --------------------------------
+// index vectors (positions, slots, lengths, page numbers) may be slices
+bool aligned_to(const void* p, uintptr_t n) { return ((uintptr_t)p & (n - 1)) == 0; }
 bool dtype_ok(int d) { return d == MX_DTYPE_F32 || d == MX_DTYPE_BF16; }
 int64_t elem_size(int d) { return d == MX_DTYPE_BF16 ? 2 : 4; }
 
@@ -274,7 +276,7 @@ int check_rope(const mx_rope* r) {
     if ((r->q_weight || r->k_weight) && (!dtype_ok(r->w_dtype) || !(r->eps >= 0.0f))) return MX_ERR_ARG;
     if (r->rot_dim && r->tokens && (!r->cos || !r->sin || !r->positions || r->table_rows < 1)) return MX_ERR_ARG;
     if (!aligned16(r->q_weight) || !aligned16(r->k_weight) || !aligned16(r->cos) || !aligned16(r->sin) ||
-        !aligned16(r->positions))
+        !aligned_to(r->positions, 4))
         return MX_ERR_ALIGN;
     return MX_OK;
 }
@@ -737,7 +739,7 @@ int mx_cache_write(const mx_kv_cache* cache, const mx_heads* k, const mx_heads* 
         if (h->heads != cache->heads || h->dtype != k->dtype) return MX_ERR_ARG;
     }
     if (!slots || tokens >= ((int64_t)1 << 30) / cache->heads) return MX_ERR_ARG;
-    if (!aligned16(slots)) return MX_ERR_ALIGN;
+    if (!aligned_to(slots, 8)) return MX_ERR_ALIGN;
     mxk::CacheWrite p;
     memset(&p, 0, sizeof(p));
     p.c = cache_params(cache);
@@ -774,7 +776,7 @@ int mx_attend(const mx_kv_cache* cache, const mx_heads* q, int64_t batch, const 
     rc = check_attend(cache, batch, q->heads, table_cols);
     if (rc) return rc;
     if (!lengths || (table_cols && !page_table) || (batch > 1 && table_stride < table_cols)) return MX_ERR_ARG;
-    if (!aligned16(lse)) return MX_ERR_ALIGN;
+    if (!aligned_to(lse, 4) || !aligned_to(lengths, 4) || !aligned_to(page_table, 4)) return MX_ERR_ALIGN;
     const size_t need = attend_bytes(cache, batch, q->heads, table_cols);
     if (need && (!workspace || ws_bytes < need)) return MX_ERR_WORKSPACE;
     if (need && !aligned16(workspace)) return MX_ERR_ALIGN;

@@ -16,9 +16,9 @@
 // inside them, the rotation in registers, and a lane's eight cosines and sines
 // are the same for every head of a token: it takes several heads of one token
 // at once, which also keeps that many loads in flight.
-// Measured (8192 tokens of 32 + 8 heads of 128, bf16, back to back): forward
-// 37 us, 4.6 TB/s; backward with its weight sums 60 us, 4.3 TB/s; a large copy
-// reaches 5.1.
+// Measured (8192 tokens of 32 + 8 heads of 128, bf16, inputs from memory):
+// forward 33.6 us, 5.1 TB/s; backward with its weight sums 58 us, 4.4 TB/s; a
+// large copy reaches 5.1.
 #include "decode_kernels.hpp"
 
 // nothing here is held to bits: fused multiply-adds are as exact and half the work
@@ -59,7 +59,23 @@ __device__ __forceinline__ void load8(float* f, const void* base, int64_t at) {
         f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w; f[4] = b.x; f[5] = b.y; f[6] = b.z; f[7] = b.w;
     }
 }
-template <bool BF>
+// A launch that writes more than the chip's L2 holds (eight times 4 MiB) writes
+// past it, backward also reads past it: forward 8192 tokens of 40 heads of 128,
+// inputs from memory, 42.9 -> 33.6 us (streamed loads as well: 36.7), backward
+// 61 -> 58; a smaller launch leaves its output where the next kernel finds it.
+constexpr int64_t STREAM_BYTES = 32 << 20;
+template <bool NT>
+__device__ __forceinline__ void put16(u32x4* p, u32x4 v) {
+    if constexpr (NT) __builtin_nontemporal_store(v, p);
+    else *p = v;
+}
+template <bool NT>
+__device__ __forceinline__ u32x4 get16(const u32x4* p) {
+    if constexpr (NT) return __builtin_nontemporal_load(p);
+    else return *p;
+}
+
+template <bool BF, bool NT>
 __device__ __forceinline__ void store8(const float* f, void* base, int64_t at) {
     if constexpr (BF) {
         u32x4 v;
@@ -71,11 +87,11 @@ __device__ __forceinline__ void store8(const float* f, void* base, int64_t at) {
             __builtin_memcpy(&w, &b, 4);
             v[e] = w;
         }
-        *reinterpret_cast<u32x4*>(static_cast<uint16_t*>(base) + at) = v;
+        put16<NT>(reinterpret_cast<u32x4*>(static_cast<uint16_t*>(base) + at), v);
     } else {
-        float4* d = reinterpret_cast<float4*>(static_cast<float*>(base) + at);
-        d[0] = make_float4(f[0], f[1], f[2], f[3]);
-        d[1] = make_float4(f[4], f[5], f[6], f[7]);
+        u32x4* d = reinterpret_cast<u32x4*>(static_cast<float*>(base) + at);
+        put16<NT>(d, u32x4{fbits(f[0]), fbits(f[1]), fbits(f[2]), fbits(f[3])});
+        put16<NT>(d + 1, u32x4{fbits(f[4]), fbits(f[5]), fbits(f[6]), fbits(f[7])});
     }
 }
 
@@ -146,7 +162,7 @@ __device__ __forceinline__ RopeSet set_of(const RopeParams& p, bool k) {
 
 // One set (queries or keys) of this launch: workgroups [b0, b0 + nb) take it.
 // LP lanes a head, HB heads of one token a lane.  dim and rot multiples of 16.
-template <bool BF, int LP, int HB>
+template <bool BF, int LP, int HB, bool NT>
 __global__ __launch_bounds__(RT) void k_rope(RopeParams p) {
     const RopeSet S = set_of(p, blockIdx.x >= p.set[0].nb);
     const uint32_t block = blockIdx.x - S.b0;
@@ -202,8 +218,8 @@ __global__ __launch_bounds__(RT) void k_rope(RopeParams p) {
         for (int h = 0; h < HB; h++) {
             if (h0 + h >= S.heads) break;
             const int64_t at = (int64_t)token * S.y_ts + (int64_t)(h0 + h) * S.y_hs;
-            store8<BF>(v[h], S.y, at + a);
-            store8<BF>(v[h] + 8, S.y, at + b);
+            store8<BF, NT>(v[h], S.y, at + a);
+            store8<BF, NT>(v[h] + 8, S.y, at + b);
         }
     }
 }
@@ -213,18 +229,18 @@ template <bool BF>
 struct Raw {
     u32x4 v[BF ? 2 : 4];
 };
-template <bool BF>
+template <bool BF, bool NT>
 __device__ __forceinline__ void load_raw(Raw<BF>& o, const void* base, int64_t at, int a, int b) {
     if constexpr (BF) {
         const uint16_t* p = static_cast<const uint16_t*>(base) + at;
-        o.v[0] = *reinterpret_cast<const u32x4*>(p + a);
-        o.v[1] = *reinterpret_cast<const u32x4*>(p + b);
+        o.v[0] = get16<NT>(reinterpret_cast<const u32x4*>(p + a));
+        o.v[1] = get16<NT>(reinterpret_cast<const u32x4*>(p + b));
     } else {
         const float* p = static_cast<const float*>(base) + at;
-        o.v[0] = *reinterpret_cast<const u32x4*>(p + a);
-        o.v[1] = *reinterpret_cast<const u32x4*>(p + a + 4);
-        o.v[2] = *reinterpret_cast<const u32x4*>(p + b);
-        o.v[3] = *reinterpret_cast<const u32x4*>(p + b + 4);
+        o.v[0] = get16<NT>(reinterpret_cast<const u32x4*>(p + a));
+        o.v[1] = get16<NT>(reinterpret_cast<const u32x4*>(p + a + 4));
+        o.v[2] = get16<NT>(reinterpret_cast<const u32x4*>(p + b));
+        o.v[3] = get16<NT>(reinterpret_cast<const u32x4*>(p + b + 4));
     }
 }
 template <bool BF>
@@ -241,7 +257,7 @@ __device__ __forceinline__ void widen(float* f, const Raw<BF>& o) {
 // them over its lanes in a fixed order and writes one partial row.  The next
 // heads are loaded, as they lie in memory, before the present ones are worked
 // on, and the position of the ones after that, which the angles' loads wait for.
-template <bool BF, int LP, int HB>
+template <bool BF, int LP, int HB, bool NT>
 __global__ __launch_bounds__(RT, 2) void k_rope_back(RopeParams p) {
     __shared__ float sh[RT / 64][16 * LP];
     const RopeSet S = set_of(p, blockIdx.x >= p.set[0].nb);
@@ -276,8 +292,8 @@ __global__ __launch_bounds__(RT, 2) void k_rope_back(RopeParams p) {
 #pragma unroll
         for (int h = 0; h < HB; h++) {
             const uint32_t hh = o.h0 + h < S.heads ? o.h0 + h : S.heads - 1;
-            load_raw(o.g[h], S.g, (int64_t)o.token * S.g_ts + (int64_t)hh * S.g_hs, a, b);
-            if (norm) load_raw(o.x[h], S.x, (int64_t)o.token * S.x_ts + (int64_t)hh * S.x_hs, a, b);
+            load_raw<BF, NT>(o.g[h], S.g, (int64_t)o.token * S.g_ts + (int64_t)hh * S.g_hs, a, b);
+            if (norm) load_raw<BF, NT>(o.x[h], S.x, (int64_t)o.token * S.x_ts + (int64_t)hh * S.x_hs, a, b);
         }
         if (p.rot) {
             const int64_t at = (o.ok ? (int64_t)pos : 0) * (p.rot / 2) + cu;
@@ -321,8 +337,8 @@ __global__ __launch_bounds__(RT, 2) void k_rope_back(RopeParams p) {
             }
             if (live && own) {
                 const int64_t at = (int64_t)o.token * S.y_ts + (int64_t)(o.h0 + h) * S.y_hs;
-                store8<BF>(g, S.y, at + a);
-                store8<BF>(g + 8, S.y, at + b);
+                store8<BF, NT>(g, S.y, at + a);
+                store8<BF, NT>(g + 8, S.y, at + b);
             }
         }
     };
@@ -522,18 +538,24 @@ uint32_t set_blocks(RopeParams& p, int lp, int hb, int64_t cap) {
     return at;
 }
 
+bool streams(const RopeParams& p, bool bf) {
+    return p.tokens * (int64_t)(p.set[0].heads + p.set[1].heads) * p.dim * (bf ? 2 : 4) > STREAM_BYTES;
+}
+
 template <bool BF, int LP, int HB>
 hipError_t forward(RopeParams& p, hipStream_t s) {
     const uint32_t n = set_blocks(p, LP, HB, 0);
     if (!n) return hipSuccess;
-    k_rope<BF, LP, HB><<<n, RT, 0, s>>>(p);
+    if (streams(p, BF)) k_rope<BF, LP, HB, true><<<n, RT, 0, s>>>(p);
+    else k_rope<BF, LP, HB, false><<<n, RT, 0, s>>>(p);
     return hipGetLastError();
 }
 template <bool BF, int LP, int HB>
 hipError_t backward(RopeParams& p, hipStream_t s) {
     const uint32_t n = set_blocks(p, LP, HB, BACK_BLOCKS);
     if (!n) return hipSuccess;
-    k_rope_back<BF, LP, HB><<<n, RT, 0, s>>>(p);
+    if (streams(p, BF)) k_rope_back<BF, LP, HB, true><<<n, RT, 0, s>>>(p);
+    else k_rope_back<BF, LP, HB, false><<<n, RT, 0, s>>>(p);
     return hipGetLastError();
 }
 // Heads per lane.  Forward: as many as leave four workgroups for each CU (bf16,

@@ -202,6 +202,19 @@ def test_long_splits(kind):
     run(kind, [5000, 1, 0, 130], 2, 1, 64, 64, torch.float32)
 
 
+@pytest.mark.parametrize("batch", [5, 64, 65, 300])
+def test_ragged_batches(batch):
+    """Many sequences of very different lengths share the workgroups: empty
+    ones, ones that fill several workgroups' shares, ones that end inside one."""
+    rng = np.random.default_rng(batch)
+    lengths = [int(v) for v in np.minimum(rng.exponential(120, batch), 900)]
+    lengths[batch // 2], lengths[0], lengths[-1] = 1500, 0, 129
+    run("bf16", lengths, 2, 1, 64, 16, torch.bfloat16, seed=batch)
+    run("mxfp8", [0] * (batch - 1) + [1300], 1, 2, 64, 32, torch.float32, seed=batch)
+    cache, table, n, q, out, lse = run("mxfp4", [0] * batch, 2, 1, 64, 16, torch.bfloat16, extra_cols=100)
+    assert (out == 0).all()
+
+
 def test_peaked_scores():
     """Scores of hundreds: the running maximum grows and old sums vanish."""
     run("bf16", [777, 200], 4, 2, 128, 16, torch.bfloat16, spread=40.0)

@@ -57,7 +57,7 @@ def call_rope(r, q=None, k=None, qo=None, ko=None):
     (dict(rot=-2), mx.MX_ERR_ARG), (dict(inter=2), mx.MX_ERR_ARG), (dict(wd=9), mx.MX_ERR_ARG),
     (dict(eps=-1.0), mx.MX_ERR_ARG), (dict(eps=float("nan")), mx.MX_ERR_ARG), (dict(cos=None), mx.MX_ERR_ARG),
     (dict(pos=None), mx.MX_ERR_ARG), (dict(rows=0), mx.MX_ERR_ARG), (dict(qw=A + 2), mx.MX_ERR_ALIGN),
-    (dict(sin=A + 4), mx.MX_ERR_ALIGN), (dict(tokens=1 << 28), mx.MX_ERR_ARG), (dict(tokens=0), mx.MX_OK),
+    (dict(sin=A + 4), mx.MX_ERR_ALIGN), (dict(pos=A + 2), mx.MX_ERR_ALIGN), (dict(tokens=1 << 28), mx.MX_ERR_ARG), (dict(tokens=0), mx.MX_OK),
 ])
 def test_rope_description(kw, status):
     assert call_rope(rope(**kw)) == status
@@ -127,6 +127,7 @@ def test_write_arguments():
     assert write(cache(), tokens=-1) == mx.MX_ERR_ARG
     assert write(cache(), tokens=0) == mx.MX_OK
     assert write(cache(), slots=None) == mx.MX_ERR_ARG
+    assert write(cache(), slots=A + 4) == mx.MX_ERR_ALIGN
     assert write(cache(), k=heads(n=7)) == mx.MX_ERR_ARG
     assert write(cache(), v=heads(dtype=0)) == mx.MX_ERR_ARG
     assert write(cache(), v=heads(x=A + 1)) == mx.MX_ERR_ALIGN
@@ -138,7 +139,8 @@ def test_attend_arguments():
     for bad in (dict(batch=-1), dict(cols=-1), dict(lengths=None), dict(table=None), dict(stride=3), dict(cols=1 << 27, stride=1 << 27),
                 dict(q=heads(n=12), out=heads(n=12)), dict(out=heads(n=8)), dict(out=heads(n=16, dtype=0))):
         assert attend(cache(), **bad) == mx.MX_ERR_ARG, bad
-    assert attend(cache(), lse=A + 4) == mx.MX_ERR_ALIGN
+    for bad in (dict(lse=A + 2), dict(lengths=A + 1), dict(table=A + 2)):
+        assert attend(cache(), **bad) == mx.MX_ERR_ALIGN, bad
     assert attend(cache(), q=heads(n=16, x=A + 4)) == mx.MX_ERR_ALIGN
     c = cache(pages=4096)
     need = mx.lib().mx_attend_workspace_size(R(c), 2, 16, 512)

@@ -205,3 +205,38 @@ def test_nothing_to_do_and_same_bits():
     first = mx.mx_matvec(f, q, x, out_dtype=torch.float32)
     for _ in range(3):
         assert torch.equal(mx.mx_matvec(f, q, x, out_dtype=torch.float32), first)
+
+
+@pytest.mark.parametrize("name,t,n,k,x_dtype", [("mxfp4", 2, 4100, 4096, torch.bfloat16), ("nvfp4", 16, 8200, 4640, torch.bfloat16),
+                                                ("int4 asym b64", 3, 4200, 9216, torch.bfloat16), ("int4 asym", 1, 40005, 1024, torch.float32),
+                                                ("mxfp4", 5, 33000, 2048, torch.float32), ("int4 b128", 9, 12400, 4096, torch.bfloat16),
+                                                ("mbs 1x16", 4, 9000, 4224, torch.bfloat16)])
+def test_many_rows(name, t, n, k, x_dtype):
+    """Workgroups of several row tiles, the last one part full, and several
+    passes over K, on random codes and scales."""
+    kw = FORMATS[name]
+    rng = np.random.default_rng(n)
+    b = kw.get("block_cols", 32)
+    codes = rng.integers(0, 256, (n, k // 2), dtype=np.uint8)
+    lo = {0: 118, 1: 40, 2: 40, 3: 100}[kw.get("scale", 0)]
+    sc = rng.integers(lo, lo + 16, (n, k // b), dtype=np.uint8)
+    off = oracle.f32_to_bf16_bits(rng.standard_normal((n, k // b)).astype(np.float32)) if kw.get("asymmetric") else None
+    mac = rng.integers(56, 65, (n, k // 128), dtype=np.uint8) if kw.get("macro_cols") else None      # 1 .. 2
+    ts = np.array([0.037], np.float32) if kw.get("scale") == 2 else None
+    val = oracle.dequantize(oracle.Format(**kw), {"codes": codes, "scales": sc, "offsets": off, "macro_scales": mac,
+                                                  "tensor_scale": ts}, n, k)
+    dev = lambda a: None if a is None else torch.from_numpy(a.view(np.int16) if a.dtype == np.uint16 else a).cuda()
+    q = mx.QTensor(n, k, dev(codes), dev(sc), offsets=dev(off), macro_scales=dev(mac), tensor_scale=dev(ts))
+    x = tokens(rng, t, k, x_dtype)
+    y = mx.mx_matvec(mx.Format(**kw), q, x, out_dtype=torch.float32)
+    w = torch.from_numpy(val).cuda().double()
+    big = w.abs()
+    if kw.get("asymmetric"):
+        big += 2 * torch.from_numpy(np.abs(oracle.bf16_bits_to_f32(off))).cuda().double().repeat_interleave(b, 1)
+    elif kw.get("elem") == 1:
+        big += 16 * torch.ldexp(torch.ones(sc.shape, device="cuda", dtype=torch.float64),
+                                dev(sc).int() - 127).repeat_interleave(b, 1)
+    want = torch.mm(x.double(), w.t().contiguous())
+    tol = (k + 64) * 2.0 ** -23 * torch.mm(x.double().abs(), big.t().contiguous())
+    err = (y.double() - want).abs()
+    assert (err <= tol).all(), f"{(err / tol).max().item():.2f} of the tolerance"

@@ -135,6 +135,31 @@ def test_many_tokens_and_weight_types(t, w_dtype):
     assert all(torch.equal(a, b) for a, b in zip(got, again)), "the same inputs gave other bits"
 
 
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_more_than_the_cache_holds(dtype):
+    """A launch that writes past L2 (over 32 MiB) and takes several heads per
+    lane gives what slices of its tokens give, bit for bit; the weight sums to
+    the rounding of their order."""
+    t, hq, hk, dim = 4700, 30, 7, 128
+    assert t * (hq + hk) * dim * 2 > 32 << 20
+    c = Case(t, hq, hk, dim, dim, dtype)
+    yq, yk = mx.mx_qk_rope(c.q, c.k, **c.args())
+    dq, dk, dqw, dkw = mx.mx_qk_rope_backward(c.dq, c.dk, c.q, c.k, **c.args())
+    sums = [torch.zeros(dim, device="cuda", dtype=torch.float64) for _ in range(2)]
+    for a in range(0, t, 470):
+        part = slice(a, a + 470)
+        args = c.args() | dict(positions=c.pos[part].contiguous())
+        sq, sk = mx.mx_qk_rope(c.q[part], c.k[part], **args)
+        assert torch.equal(sq, yq[part]) and torch.equal(sk, yk[part])
+        gq, gk, gqw, gkw = mx.mx_qk_rope_backward(c.dq[part], c.dk[part], c.q[part], c.k[part], **args)
+        assert torch.equal(gq, dq[part]) and torch.equal(gk, dk[part])
+        sums[0] += gqw.double()
+        sums[1] += gkw.double()
+    for dw, total, dy, x, w in ((dqw, sums[0], c.dq, c.q, c.qw), (dkw, sums[1], c.dk, c.k, c.kw)):
+        wmag = c.backward64(dy, x, w)[3]
+        near(dw, total.cpu().numpy(), 2 * (t * x.shape[1] + dim + 64) * U * wmag, "dw")
+
+
 @pytest.mark.parametrize("dim,rot", [(128, 128), (80, 40)])
 def test_in_place_queries_only_and_mixed_weights(dim, rot):
     c = Case(21, 6, 2, dim, rot, torch.bfloat16)
