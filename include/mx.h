@@ -321,7 +321,7 @@ int mx_gemm(const mx_format *fa, const mx_qtensor *a, const mx_format *fb,
  *  - A NaN scale code makes its row's outputs NaN, a NaN or Inf in a token
  *    makes that token's outputs non-finite, other tokens are untouched.
  *  - Any number of tokens runs; the kernel is made for up to 16 (more read the
- *    weight once per 16).  w->rows < 2^31, 0 < w->cols < 2^27, tokens <= 2^20.
+ *    weight once per 16).  w->rows < 2^31, 0 < w->cols < 2^24, tokens <= 1048560.
  *  - x, W's buffers, bias and y 16-byte aligned, ldx a multiple of 16 bytes
  *    (MX_ERR_ALIGN).  y must not overlap an input.                           */
 int mx_matvec(const mx_format *fw, const mx_qtensor *w, int x_dtype, const void *x, int64_t tokens,

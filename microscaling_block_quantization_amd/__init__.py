@@ -551,7 +551,7 @@ def mx_qk_rope_backward(dy_q, dy_k, q, k, cos, sin, positions, q_weight=None, k_
     return dq, dk, dqw, dkw
 
 
-@dataclass(frozen=True)
+@dataclass(frozen=True, eq=False)
 class KVCache:
     """A paged cache of keys and values.  fmt None: k and v are bf16, pages x
     heads x page_size x dim.  fmt MXFP8_E4M3 or MXFP4: uint8 codes, pages x

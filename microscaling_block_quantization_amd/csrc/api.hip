@@ -615,7 +615,7 @@ int mx_matvec(const mx_format* fw, const mx_qtensor* w, int x_dtype, const void*
         return MX_ERR_UNSUPPORTED;
     if (!dtype_ok(x_dtype) || !dtype_ok(y_dtype) || tokens < 0) return MX_ERR_ARG;
     const int64_t N = w->rows, K = w->cols;
-    if (ldx < K || ldy < N || N >= (int64_t)1 << 31 || K >= (int64_t)1 << 27 || tokens > (int64_t)1 << 20) return MX_ERR_ARG;
+    if (ldx < K || ldy < N || N >= (int64_t)1 << 31 || K >= (int64_t)1 << 24 || tokens > (int64_t)16 * 65535) return MX_ERR_ARG;
     if (N == 0 || tokens == 0) return MX_OK;
     if (K == 0) return MX_ERR_UNSUPPORTED;
     if (!x || !y || !w->codes || !w->scales) return MX_ERR_ARG;

@@ -28,7 +28,8 @@ def matvec(kw=None, rows=64, cols=256, xd=1, x=A, tokens=1, ldx=256, bias=None, 
     (dict(macro_cols=128), {}, mx.MX_ERR_ARG), (dict(scale=2, block_cols=16), {}, mx.MX_ERR_ARG),
     ({}, dict(x=A + 8), mx.MX_ERR_ALIGN), ({}, dict(y=A + 2), mx.MX_ERR_ALIGN), ({}, dict(bias=A + 4), mx.MX_ERR_ALIGN),
     ({}, dict(codes=A + 4), mx.MX_ERR_ALIGN), ({}, dict(ldx=260), mx.MX_ERR_ALIGN),
-    ({}, dict(cols=0, ldx=8), mx.MX_ERR_UNSUPPORTED), ({}, dict(tokens=1 << 40), mx.MX_ERR_ARG),
+    ({}, dict(cols=0, ldx=8), mx.MX_ERR_UNSUPPORTED), ({}, dict(tokens=1048561), mx.MX_ERR_ARG),
+    ({}, dict(cols=1 << 24, ldx=1 << 24), mx.MX_ERR_ARG),
     ({}, dict(tokens=0), mx.MX_OK), ({}, dict(rows=0), mx.MX_OK),
 ])
 def test_matvec(kw, args, status):
