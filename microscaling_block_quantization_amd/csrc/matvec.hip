@@ -37,7 +37,12 @@
 // (4.0); NVFP4 16 x 28672 x 8192 39.9 (3.3), where its exact fp32 decode (16
 // vector operations per 8 codes) is half the vector unit's time.  Loading the
 // same bytes alone takes 25 us.  Tried: x through LDS in chunks 58 us, x loaded
-// per step 52 to 83, sixteen waves 42, codes two tiles ahead 42.
+// per step 52 to 83, sixteen waves 42, codes two tiles ahead 42.  The next
+// pass's x and codes under this pass's last tile: 12.3 us against 12.6 at MXFP4
+// 1 x 4096 x 14336, and fp32 tokens out of registers.  fp32 tokens take 17.6 us at
+// MXFP4 1 x 14336 x 4096; their three parts side by side in the columns instead of
+// in three products: 20.9 against 18.2 for five tokens, 48 against 52 for NVFP4
+// 2 x 28672 x 8192.
 #include <type_traits>
 
 #include "decode_kernels.hpp"
