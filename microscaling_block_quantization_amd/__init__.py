@@ -392,7 +392,8 @@ def mx_gemm(fa: Format, a: QTensor, fb: Format, b: QTensor, c=None, out_dtype=to
 # ---- one decode step with quantized weights and a quantized cache ------------
 # These kernels take a few microseconds, so the host's share of a call counts:
 # each check is one cheap comparison whose message is only formed when it
-# fails, and structs are packed as bytes.
+# fails, and structs are packed as bytes.  `stream`: the stream to launch on
+# (default: the current one), see _on.
 _DTYPES = {torch.float32: DTYPE_F32, torch.bfloat16: DTYPE_BF16}
 _PACK_FORMAT = struct.Struct("@9if2Q").pack
 _PACK_QTENSOR = struct.Struct("@6P2q").pack
@@ -407,10 +408,29 @@ def _code(dtype):
         raise TypeError(f"unsupported dtype {dtype}") from None
 
 
-def _stream_ptr(stream):
-    if stream is None:
-        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
-    return stream.cuda_stream
+def _on(stream, call, *args):
+    """call(*args) with `stream` as the current stream, so that what the call
+    allocates belongs to the stream its kernels run on: a workspace freed at
+    the return, and an output, are given out again in that stream's order.  The
+    outputs' use on the caller's stream is recorded."""
+    caller = torch.cuda.current_stream(stream.device)
+    with torch.cuda.stream(stream):
+        out = call(*args)
+    if stream != caller:
+        _record(out, caller)
+    return out
+
+
+def _record(out, stream):
+    if isinstance(out, torch.Tensor):
+        out.record_stream(stream)
+    elif isinstance(out, (tuple, list)):
+        for o in out:
+            _record(o, stream)
+
+
+def _stream_ptr():
+    return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
 
 
 def _raw(t):
@@ -437,6 +457,8 @@ def mx_matvec(fmt: Format, w: QTensor, x: torch.Tensor, bias=None, y=None, out_d
     or fp32, any row stride) and a 4-bit weight W (N x K: E2M1 or INT4 in row
     blocks, see include/mx.h).  bias: None or N values of x's dtype.  y: a
     tokens x N view to write into, else a new tensor of out_dtype (default: x's)."""
+    if stream is not None:
+        return _on(stream, mx_matvec, fmt, w, x, bias, y, out_dtype)
     n, k = w.rows, w.cols
     if x.dim() != 2 or x.size(1) != k or x.get_device() != w.codes.get_device():
         raise ValueError(f"mx_matvec: x must be tokens x {k} on the weight's device")
@@ -458,7 +480,7 @@ def mx_matvec(fmt: Format, w: QTensor, x: torch.Tensor, bias=None, y=None, out_d
                      fmt.macro_cols, fmt.oas_tau, fmt.seed, fmt.rng_offset)
     q = _PACK_QTENSOR(w.codes.data_ptr(), w.scales.data_ptr(), _raw(w.offsets), _raw(w.macro_scales), _raw(w.tensor_scale), 0, n, k)
     _check(lib().mx_matvec(f, q, _code(x.dtype), x.data_ptr(), tokens, ldx, bp, y.data_ptr(), ldy, _code(y.dtype),
-                           _stream_ptr(stream)), "mx_matvec")
+                           _stream_ptr()), "mx_matvec")
     return y
 
 
@@ -504,6 +526,8 @@ def mx_qk_rope(q, k, cos, sin, positions, q_weight=None, k_weight=None, eps=1e-6
     pairs (2i, 2i+1) instead of (i, i + rot_dim/2).  q_out, k_out: tensors to
     write into (q and k themselves included), else new ones.
     Returns (q_out, k_out)."""
+    if stream is not None:
+        return _on(stream, mx_qk_rope, q, k, cos, sin, positions, q_weight, k_weight, eps, interleaved, q_out, k_out)
     if q.dim() != 3:
         raise ValueError("mx_qk_rope: q must be tokens x heads x dim")
     dev, dim = q.get_device(), q.size(2)
@@ -514,7 +538,7 @@ def mx_qk_rope(q, k, cos, sin, positions, q_weight=None, k_weight=None, eps=1e-6
     if k is not None:
         hk = _heads(k, dim, dev, "mx_qk_rope: k")
         k_out, ok = _out_heads(k_out, k, dim, dev, "mx_qk_rope: k_out")
-    _check(lib().mx_qk_rope(r, hq, hk, oq, ok, _stream_ptr(stream)), "mx_qk_rope")
+    _check(lib().mx_qk_rope(r, hq, hk, oq, ok, _stream_ptr()), "mx_qk_rope")
     return q_out, k_out
 
 
@@ -530,6 +554,9 @@ def mx_qk_rope_backward(dy_q, dy_k, q, k, cos, sin, positions, q_weight=None, k_
     """Gradient of mx_qk_rope: dy_q, dy_k are the gradients of its outputs, the
     rest are its arguments.  Returns (dq, dk, dq_weight, dk_weight); the weight
     gradients are fp32 (None without that weight).  dq, dk may be dy_q, dy_k."""
+    if stream is not None:
+        return _on(stream, mx_qk_rope_backward, dy_q, dy_k, q, k, cos, sin, positions, q_weight, k_weight, eps, interleaved, dq, dk,
+                   workspace)
     if q.dim() != 3 or (k is None) != (dy_k is None):
         raise ValueError("mx_qk_rope_backward: q must be tokens x heads x dim, and dy_k and k go together")
     dev, dim = q.get_device(), q.size(2)
@@ -547,7 +574,7 @@ def mx_qk_rope_backward(dy_q, dy_k, q, k, cos, sin, positions, q_weight=None, k_
     if workspace is None and (dqw is not None or dkw is not None):
         workspace = cos.new_empty((lib().mx_qk_rope_workspace_size(r),), dtype=torch.uint8)
     _check(lib().mx_qk_rope_backward(r, gq, gk, xq, xk, oq, ok, _raw(dqw), _raw(dkw), _raw(workspace),
-                                     0 if workspace is None else workspace.numel(), _stream_ptr(stream)), "mx_qk_rope_backward")
+                                     0 if workspace is None else workspace.numel(), _stream_ptr()), "mx_qk_rope_backward")
     return dq, dk, dqw, dkw
 
 
@@ -608,13 +635,15 @@ def mx_cache_write(cache: KVCache, k, v, slots, stream=None):
     fp32, any token and head strides) to the cache, quantized to its format.
     slots: int64 per token, page * page_size + position in the page; a slot
     outside the cache skips its token.  Returns the cache."""
+    if stream is not None:
+        return _on(stream, mx_cache_write, cache, k, v, slots)
     dev, dim = cache.k.get_device(), cache.dim
     hk, hv = _heads(k, dim, dev, "mx_cache_write: k"), _heads(v, dim, dev, "mx_cache_write: v")
     tokens = k.size(0)
     if v.size(0) != tokens:
         raise ValueError("mx_cache_write: k and v differ in tokens")
     at = _vector(slots, tokens, torch.int64, dev, "mx_cache_write", "slots")
-    _check(lib().mx_cache_write(cache._ref, hk, hv, tokens, at, _stream_ptr(stream)), "mx_cache_write")
+    _check(lib().mx_cache_write(cache._ref, hk, hv, tokens, at, _stream_ptr()), "mx_cache_write")
     return cache
 
 
@@ -634,6 +663,8 @@ def mx_attend(q, cache: KVCache, page_table, lengths, scale=None, out=None, lse=
     (allocate) or a batch x heads fp32 tensor.  workspace: as
     alloc_attend_workspace gives (allocated when None).
     Returns out, or (out, lse) when lse is asked for."""
+    if stream is not None:
+        return _on(stream, mx_attend, q, cache, page_table, lengths, scale, out, lse, workspace)
     dev, dim = cache.k.get_device(), cache.dim
     hq = _heads(q, dim, dev, "mx_attend: q")
     batch, heads = q.size(0), q.size(1)
@@ -654,5 +685,5 @@ def mx_attend(q, cache: KVCache, page_table, lengths, scale=None, out=None, lse=
         workspace = cache.k.new_empty((lib().mx_attend_workspace_size(cache._ref, batch, heads, cols),), dtype=torch.uint8)
     _check(lib().mx_attend(cache._ref, hq, batch, page_table.data_ptr(), cols, cols if batch <= 1 else stride, n,
                            dim ** -0.5 if scale is None else scale, ho, _raw(lse), workspace.data_ptr(), workspace.numel(),
-                           _stream_ptr(stream)), "mx_attend")
+                           _stream_ptr()), "mx_attend")
     return out if lse is None else (out, lse)
