@@ -199,10 +199,31 @@ def _ptr(t):
     return None if t is None else ctypes.c_void_p(t.data_ptr())
 
 
-def _stream(stream):
-    if stream is None:
-        stream = torch.cuda.current_stream()
-    return ctypes.c_void_p(stream.cuda_stream)
+def _on(stream, call, *args):
+    """call(*args) with `stream` as the current stream, so that what the call
+    allocates belongs to the stream its kernels run on: a workspace freed at
+    the return, and an output, are given out again in that stream's order.  The
+    outputs' use on the caller's stream is recorded."""
+    caller = torch.cuda.current_stream(stream.device)
+    with torch.cuda.stream(stream):
+        out = call(*args)
+    if stream != caller:
+        _record(out, caller)
+    return out
+
+
+def _record(out, stream):
+    if isinstance(out, torch.Tensor):
+        out.record_stream(stream)
+    elif isinstance(out, QTensor):
+        _record((out.codes, out.scales, out.offsets, out.macro_scales, out.tensor_scale, out.ref_exp), stream)
+    elif isinstance(out, (tuple, list)):
+        for o in out:
+            _record(o, stream)
+
+
+def _stream():
+    return ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
 
 
 def _check(rc, where):
@@ -262,6 +283,8 @@ def mx_quantize(fmt: Format, x: torch.Tensor, out: QTensor = None, dequant=None,
     dequant: None, a dtype (torch.float32 / torch.bfloat16) to allocate, or a tensor.
     stats: None, True (allocate), or a 48-byte device uint8 tensor.
     Returns (qtensor, dequant tensor or None, stats tensor or None)."""
+    if stream is not None:
+        return _on(stream, mx_quantize, fmt, x, out, dequant, stats, workspace)
     assert x.dim() == 2 and x.is_cuda
     rows, cols = x.shape
     ld = x.stride(0) if rows > 1 else cols
@@ -280,7 +303,7 @@ def mx_quantize(fmt: Format, x: torch.Tensor, out: QTensor = None, dequant=None,
     rc = lib().mx_quantize(ctypes.byref(f), _dtype_code(x), _ptr(x), rows, cols, ld, ctypes.byref(q),
                            _ptr(dequant), DTYPE_F32 if dequant is None else _dtype_code(dequant),
                            _ptr(stats), _ptr(workspace),
-                           0 if workspace is None else workspace.numel(), _stream(stream))
+                           0 if workspace is None else workspace.numel(), _stream())
     _check(rc, "mx_quantize")
     return out, dequant, stats
 
@@ -292,6 +315,8 @@ def mx_quantize_noalloc(fmt: Format, x: torch.Tensor, out: QTensor, dequant=None
     outputs are the caller's: `out` (a QTensor), `dequant` (None or a tensor)
     and `stats` (None or a 48-byte device tensor).  Calls that overlap on one
     GPU share the array and race."""
+    if stream is not None:
+        return _on(stream, mx_quantize_noalloc, fmt, x, out, dequant, stats)
     assert x.dim() == 2 and x.is_cuda and x.stride(1) == 1
     rows, cols = x.shape
     ld = x.stride(0) if rows > 1 else cols
@@ -299,7 +324,7 @@ def mx_quantize_noalloc(fmt: Format, x: torch.Tensor, out: QTensor, dequant=None
     q = out.c()
     rc = lib().mx_quantize_noalloc(ctypes.byref(f), _dtype_code(x), _ptr(x), rows, cols, ld, ctypes.byref(q),
                                    _ptr(dequant), DTYPE_F32 if dequant is None else _dtype_code(dequant),
-                                   _ptr(stats), _stream(stream))
+                                   _ptr(stats), _stream())
     _check(rc, "mx_quantize_noalloc")
     return out, dequant, stats
 
@@ -310,6 +335,8 @@ def mx_quantize_many(fmt: Format, xs, outs=None, stats=None, workspaces=None, st
     True (allocate one per tensor) or a list of 48-byte device tensors (or
     None entries); workspaces: None (allocated where needed) or a list.
     Returns (list of qtensors, list of stats tensors or None)."""
+    if stream is not None:
+        return _on(stream, mx_quantize_many, fmt, xs, outs, stats, workspaces)
     xs = list(xs)
     n = len(xs)
     outs = [None] * n if outs is None else list(outs)
@@ -337,18 +364,20 @@ def mx_quantize_many(fmt: Format, xs, outs=None, stats=None, workspaces=None, st
                          None if stats[i] is None else stats[i].data_ptr(),
                          None if ws is None else ws.data_ptr(), 0 if ws is None else ws.numel())
     f = fmt.c()
-    rc = lib().mx_quantize_many(ctypes.byref(f), dt, jobs, n, _stream(stream))
+    rc = lib().mx_quantize_many(ctypes.byref(f), dt, jobs, n, _stream())
     _check(rc, "mx_quantize_many")
     return outs, stats
 
 
 def mx_dequantize(fmt: Format, q: QTensor, out_dtype=torch.float32, y=None, stream=None):
+    if stream is not None:
+        return _on(stream, mx_dequantize, fmt, q, out_dtype, y)
     if y is None:
         y = torch.empty((q.rows, q.cols), dtype=out_dtype, device=q.codes.device)
     f = fmt.c()
     qc = q.c()
     ld = y.stride(0) if q.rows > 1 else q.cols
-    rc = lib().mx_dequantize(ctypes.byref(f), ctypes.byref(qc), _dtype_code(y), _ptr(y), ld, _stream(stream))
+    rc = lib().mx_dequantize(ctypes.byref(f), ctypes.byref(qc), _dtype_code(y), _ptr(y), ld, _stream())
     _check(rc, "mx_dequantize")
     return y
 
@@ -359,6 +388,8 @@ def mx_qsnr_workspace_size(n):
 
 def mx_qsnr(ref: torch.Tensor, approx: torch.Tensor, workspace=None, stream=None):
     """QSNR (dB) of eq. (1)/(2) between two device tensors; returns (stats, dB)."""
+    if stream is not None:
+        return _on(stream, mx_qsnr, ref, approx, workspace)
     assert ref.dtype == approx.dtype and ref.numel() == approx.numel()
     assert ref.is_contiguous() and approx.is_contiguous()
     n = ref.numel()
@@ -367,7 +398,7 @@ def mx_qsnr(ref: torch.Tensor, approx: torch.Tensor, workspace=None, stream=None
     st = MxStats()
     d = ctypes.c_double()
     rc = lib().mx_qsnr(_dtype_code(ref), _ptr(ref), _ptr(approx), n, ctypes.byref(st), ctypes.byref(d),
-                       _ptr(workspace), workspace.numel(), _stream(stream))
+                       _ptr(workspace), workspace.numel(), _stream())
     _check(rc, "mx_qsnr")
     return {k: getattr(st, k) for k, _ in MxStats._fields_}, d.value
 
@@ -378,13 +409,15 @@ def mx_gemm(fa: Format, a: QTensor, fb: Format, b: QTensor, c=None, out_dtype=to
     carry 1 x 128 macro-block scales, macro_cols=128); or E2M1 under UE4M3,
     NVFP4, UE5M3 or E8M0 scales on other row blocks.  c: an M x N view (any
     row stride) to write into, else a new tensor of out_dtype."""
+    if stream is not None:
+        return _on(stream, mx_gemm, fa, a, fb, b, c, out_dtype)
     if c is None:
         c = torch.empty((a.rows, b.rows), dtype=out_dtype, device=a.codes.device)
     ldc = c.stride(0) if a.rows > 1 else b.rows
     f1, f2 = fa.c(), fb.c()
     qa, qb = a.c(), b.c()
     rc = lib().mx_gemm(ctypes.byref(f1), ctypes.byref(qa), ctypes.byref(f2), ctypes.byref(qb), _ptr(c), ldc,
-                       _dtype_code(c), _stream(stream))
+                       _dtype_code(c), _stream())
     _check(rc, "mx_gemm")
     return c
 
@@ -406,27 +439,6 @@ def _code(dtype):
         return _DTYPES[dtype]
     except KeyError:
         raise TypeError(f"unsupported dtype {dtype}") from None
-
-
-def _on(stream, call, *args):
-    """call(*args) with `stream` as the current stream, so that what the call
-    allocates belongs to the stream its kernels run on: a workspace freed at
-    the return, and an output, are given out again in that stream's order.  The
-    outputs' use on the caller's stream is recorded."""
-    caller = torch.cuda.current_stream(stream.device)
-    with torch.cuda.stream(stream):
-        out = call(*args)
-    if stream != caller:
-        _record(out, caller)
-    return out
-
-
-def _record(out, stream):
-    if isinstance(out, torch.Tensor):
-        out.record_stream(stream)
-    elif isinstance(out, (tuple, list)):
-        for o in out:
-            _record(o, stream)
 
 
 def _stream_ptr():

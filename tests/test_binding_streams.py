@@ -82,12 +82,15 @@ def addresses(args):
                 yield from (v for v in (getattr(e, n) for n, _ in e._fields_) if isinstance(v, int))
 
 
+def number(stream):
+    return stream.value if isinstance(stream, ctypes.c_void_p) else stream
+
+
 def check(machine, call):
     side = Stream(2)
     out = call(side)
     (name, args), = machine.launches
-    last = args[-1]
-    assert (last.value if isinstance(last, ctypes.c_void_p) else last) == 2, "launched on another stream"
+    assert number(args[-1]) == 2, "launched on another stream"
     used = {a for a in addresses(args) if a in machine.allocated}
     assert used, "the call allocated nothing, so the test shows nothing"
     for a in used:
@@ -106,5 +109,42 @@ def test_decode_calls(machine, call):
 def test_the_current_stream_given_by_name(machine, call):
     """Same stream, nothing to record."""
     out = call(Stream(1))
-    assert machine.launches[0][1][-1] == 1
+    assert number(machine.launches[0][1][-1]) == 1
     assert all(not getattr(t, "recorded", ()) for t in tensors(out))
+
+
+# ---- quantization, its inverse, statistics, the large product -------------------
+STATS = mx.Format(scale=mx.SCALE_NVFP4, block_cols=16)
+
+
+def quantize(stream):
+    return mx.mx_quantize(STATS, heads(1, 64, 128)[0], dequant=torch.float32, stats=True, stream=stream)
+
+
+def quantize_many(stream):
+    outs, stats = mx.mx_quantize_many(STATS, [heads(1, 64, 128)[0], heads(1, 32, 64)[0]], stats=True, stream=stream)
+    return outs + stats
+
+
+def dequantize(stream):
+    return mx.mx_dequantize(mx.MXFP4, weight(), stream=stream)
+
+
+def gemm(stream):
+    return mx.mx_gemm(mx.MXFP4, weight(32), mx.MXFP4, weight(64), stream=stream)
+
+
+def qsnr(stream):
+    return mx.mx_qsnr(heads(1, 64, 128)[0], heads(1, 64, 128)[0], stream=stream)
+
+
+@pytest.mark.parametrize("call", [quantize, quantize_many, dequantize, gemm, qsnr])
+def test_other_calls(machine, call):
+    check(machine, call)
+
+
+def test_quantize_noalloc_allocates_nothing(machine):
+    q = mx.alloc_qtensor(mx.MXFP4, 64, 256)
+    made = len(machine.allocated)
+    out, _, _ = mx.mx_quantize_noalloc(mx.MXFP4, heads(1, 64, 256)[0], q, stream=Stream(2))
+    assert out is q and len(machine.allocated) == made and number(machine.launches[0][1][-1]) == 2

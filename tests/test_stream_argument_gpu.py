@@ -80,3 +80,31 @@ def test_many_calls_on_a_side_stream():
         torch.full((1 << 16,), float("nan"), device="cuda")
     main.wait_stream(side)
     assert all(torch.equal(a, b) for o in outs for a, b in zip(o, want))
+
+
+NVFP4 = mx.Format(scale=mx.SCALE_NVFP4, block_cols=16)
+
+
+def test_quantize_and_products():
+    """The calls around quantization on a side stream: results as on the
+    current one, new tensors in the side stream's pool."""
+    x, w = rnd(96, 512), rnd(64, 512)
+
+    def all_of(**s):
+        q, dq, st = mx.mx_quantize(NVFP4, x, dequant=torch.float32, stats=True, **s)
+        (a, b), sts = mx.mx_quantize_many(mx.MXFP4, [x, w], stats=True, **s)
+        return [q.codes, q.scales, q.tensor_scale, dq, st, a.codes, b.scales, sts[0], sts[1],
+                mx.mx_dequantize(NVFP4, q, **s), mx.mx_gemm(mx.MXFP4, a, mx.MXFP4, b, **s),
+                mx.mx_matvec(mx.MXFP4, b, x[:3], **s)]
+
+    want = all_of()
+    side, main = torch.cuda.Stream(), torch.cuda.current_stream()
+    side.wait_stream(main)
+    got = all_of(stream=side)
+    main.wait_stream(side)
+    for i, (a, b) in enumerate(zip(got, want)):
+        n = 48 if i in (4, 7, 8) else a.numel()                # mx_stats are 48 bytes
+        assert torch.equal(a.view(-1)[:n], b.view(-1)[:n]), i
+        assert pool_of(a.data_ptr()) == side.cuda_stream, i
+    err, db = mx.mx_qsnr(x, x.clone(), stream=side)
+    assert err["n"] == x.numel()
