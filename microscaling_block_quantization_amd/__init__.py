@@ -441,7 +441,10 @@ def _code(dtype):
         raise TypeError(f"unsupported dtype {dtype}") from None
 
 
-def _stream_ptr():
+def _stream_ptr(dev, where):
+    """The stream of a launch whose operands lie on device `dev`."""
+    if dev < 0:
+        raise ValueError(f"{where}: the operands must be GPU tensors")
     return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
 
 
@@ -462,6 +465,20 @@ def _vector(t, n, dtype, dev, where, name):
     if t.shape != (n,) or not t.is_contiguous() or t.get_device() != dev or (dtype is not None and t.dtype != dtype):
         raise ValueError(f"{where}: {name} must be {n} contiguous values{'' if dtype is None else f' of {dtype}'} on the inputs' device")
     return t.data_ptr()
+
+
+def _buffer(t, dev, where, name):
+    """The address of a caller's buffer (0: none)."""
+    if t is None:
+        return 0
+    if t.get_device() != dev or not t.is_contiguous():
+        raise ValueError(f"{where}: {name} must be contiguous and on the inputs' device")
+    return t.data_ptr()
+
+
+def _workspace(t, dev, where):
+    """The address and bytes of a workspace."""
+    return _buffer(t, dev, where, "workspace"), 0 if t is None else t.nbytes
 
 
 def mx_matvec(fmt: Format, w: QTensor, x: torch.Tensor, bias=None, y=None, out_dtype=None, stream=None):
@@ -490,9 +507,11 @@ def mx_matvec(fmt: Format, w: QTensor, x: torch.Tensor, bias=None, y=None, out_d
         ldx, ldy = k, n
     f = _PACK_FORMAT(fmt.elem, fmt.scale, fmt.rule, fmt.round, fmt.block_rows, fmt.block_cols, fmt.asymmetric, fmt.hadamard,
                      fmt.macro_cols, fmt.oas_tau, fmt.seed, fmt.rng_offset)
-    q = _PACK_QTENSOR(w.codes.data_ptr(), w.scales.data_ptr(), _raw(w.offsets), _raw(w.macro_scales), _raw(w.tensor_scale), 0, n, k)
+    at = lambda t, name: _buffer(t, dev, "mx_matvec", name)
+    q = _PACK_QTENSOR(at(w.codes, "codes"), at(w.scales, "scales"), at(w.offsets, "offsets"), at(w.macro_scales, "macro_scales"),
+                      at(w.tensor_scale, "tensor_scale"), 0, n, k)
     _check(lib().mx_matvec(f, q, _code(x.dtype), x.data_ptr(), tokens, ldx, bp, y.data_ptr(), ldy, _code(y.dtype),
-                           _stream_ptr()), "mx_matvec")
+                           _stream_ptr(dev, "mx_matvec")), "mx_matvec")
     return y
 
 
@@ -550,7 +569,7 @@ def mx_qk_rope(q, k, cos, sin, positions, q_weight=None, k_weight=None, eps=1e-6
     if k is not None:
         hk = _heads(k, dim, dev, "mx_qk_rope: k")
         k_out, ok = _out_heads(k_out, k, dim, dev, "mx_qk_rope: k_out")
-    _check(lib().mx_qk_rope(r, hq, hk, oq, ok, _stream_ptr()), "mx_qk_rope")
+    _check(lib().mx_qk_rope(r, hq, hk, oq, ok, _stream_ptr(dev, "mx_qk_rope")), "mx_qk_rope")
     return q_out, k_out
 
 
@@ -585,8 +604,9 @@ def mx_qk_rope_backward(dy_q, dy_k, q, k, cos, sin, positions, q_weight=None, k_
     dkw = None if k_weight is None else cos.new_empty((dim,))
     if workspace is None and (dqw is not None or dkw is not None):
         workspace = cos.new_empty((lib().mx_qk_rope_workspace_size(r),), dtype=torch.uint8)
-    _check(lib().mx_qk_rope_backward(r, gq, gk, xq, xk, oq, ok, _raw(dqw), _raw(dkw), _raw(workspace),
-                                     0 if workspace is None else workspace.numel(), _stream_ptr()), "mx_qk_rope_backward")
+    ws, nbytes = _workspace(workspace, dev, "mx_qk_rope_backward")
+    _check(lib().mx_qk_rope_backward(r, gq, gk, xq, xk, oq, ok, _raw(dqw), _raw(dkw), ws, nbytes,
+                                     _stream_ptr(dev, "mx_qk_rope_backward")), "mx_qk_rope_backward")
     return dq, dk, dqw, dkw
 
 
@@ -617,7 +637,7 @@ class KVCache:
             grid = (pages, heads, page_size, dim // 32)
             need += [(self.k_scales, grid, torch.uint8), (self.v_scales, grid, torch.uint8)]
         for t, shape, dt in need:
-            if t is None or t.shape != shape or t.dtype != dt or not t.is_contiguous() or t.device != self.k.device:
+            if t is None or t.shape != shape or t.dtype != dt or not t.is_contiguous() or t.get_device() != self.k.get_device():
                 raise ValueError(f"KVCache: expected a contiguous {dt} buffer of {tuple(shape)}")
         for name, v in (("pages", pages), ("heads", heads), ("page_size", page_size), ("dim", dim)):
             put(name, v)
@@ -655,7 +675,7 @@ def mx_cache_write(cache: KVCache, k, v, slots, stream=None):
     if v.size(0) != tokens:
         raise ValueError("mx_cache_write: k and v differ in tokens")
     at = _vector(slots, tokens, torch.int64, dev, "mx_cache_write", "slots")
-    _check(lib().mx_cache_write(cache._ref, hk, hv, tokens, at, _stream_ptr()), "mx_cache_write")
+    _check(lib().mx_cache_write(cache._ref, hk, hv, tokens, at, _stream_ptr(dev, "mx_cache_write")), "mx_cache_write")
     return cache
 
 
@@ -695,7 +715,8 @@ def mx_attend(q, cache: KVCache, page_table, lengths, scale=None, out=None, lse=
         raise ValueError(f"mx_attend: lse must be a contiguous fp32 {batch} x {heads}")
     if workspace is None:
         workspace = cache.k.new_empty((lib().mx_attend_workspace_size(cache._ref, batch, heads, cols),), dtype=torch.uint8)
+    ws, nbytes = _workspace(workspace, dev, "mx_attend")
     _check(lib().mx_attend(cache._ref, hq, batch, page_table.data_ptr(), cols, cols if batch <= 1 else stride, n,
-                           dim ** -0.5 if scale is None else scale, ho, _raw(lse), workspace.data_ptr(), workspace.numel(),
-                           _stream_ptr()), "mx_attend")
+                           dim ** -0.5 if scale is None else scale, ho, _raw(lse), ws, nbytes,
+                           _stream_ptr(dev, "mx_attend")), "mx_attend")
     return out if lse is None else (out, lse)

@@ -41,7 +41,8 @@ class OnGpu(torch.Tensor):
             kwargs["device"] = "cpu"
         out = super().__torch_function__(func, types, args, kwargs)
         if isinstance(out, torch.Tensor) and func in (torch.Tensor.new_empty, torch.empty_like):
-            cls.now.made(out.as_subclass(OnGpu))
+            out.card = args[0].card
+            cls.now.made(out)
         return out
 
 
