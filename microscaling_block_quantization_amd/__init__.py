@@ -467,18 +467,18 @@ def _vector(t, n, dtype, dev, where, name):
     return t.data_ptr()
 
 
-def _buffer(t, dev, where, name):
-    """The address of a caller's buffer (0: none)."""
+def _buffer(t, nbytes, dev, where, name):
+    """The address of a caller's buffer of at least nbytes (0: none)."""
     if t is None:
         return 0
-    if t.get_device() != dev or not t.is_contiguous():
-        raise ValueError(f"{where}: {name} must be contiguous and on the inputs' device")
+    if t.nbytes < nbytes or t.get_device() != dev or not t.is_contiguous():
+        raise ValueError(f"{where}: {name} must be {nbytes} contiguous bytes at least, on the inputs' device")
     return t.data_ptr()
 
 
 def _workspace(t, dev, where):
     """The address and bytes of a workspace."""
-    return _buffer(t, dev, where, "workspace"), 0 if t is None else t.nbytes
+    return _buffer(t, 0, dev, where, "workspace"), 0 if t is None else t.nbytes
 
 
 def mx_matvec(fmt: Format, w: QTensor, x: torch.Tensor, bias=None, y=None, out_dtype=None, stream=None):
@@ -507,9 +507,20 @@ def mx_matvec(fmt: Format, w: QTensor, x: torch.Tensor, bias=None, y=None, out_d
         ldx, ldy = k, n
     f = _PACK_FORMAT(fmt.elem, fmt.scale, fmt.rule, fmt.round, fmt.block_rows, fmt.block_cols, fmt.asymmetric, fmt.hadamard,
                      fmt.macro_cols, fmt.oas_tau, fmt.seed, fmt.rng_offset)
-    at = lambda t, name: _buffer(t, dev, "mx_matvec", name)
-    q = _PACK_QTENSOR(at(w.codes, "codes"), at(w.scales, "scales"), at(w.offsets, "offsets"), at(w.macro_scales, "macro_scales"),
-                      at(w.tensor_scale, "tensor_scale"), 0, n, k)
+    # row blocks of 4-bit codes: any other format is the library's to refuse
+    held = n * k if fmt.block_rows == 1 and fmt.block_cols > 0 and fmt.elem in (ELEM_E2M1, ELEM_INT4) else 0
+    blocks = held // (fmt.block_cols or 1)
+    offsets = macro = ts = 0
+    if w.offsets is not None:
+        offsets = _buffer(w.offsets, 2 * blocks if fmt.asymmetric else 0, dev, "mx_matvec", "offsets")
+    if w.macro_scales is not None:
+        macro = _buffer(w.macro_scales, held // 128 if fmt.macro_cols else 0, dev, "mx_matvec", "macro_scales")
+    if w.tensor_scale is not None:
+        if w.tensor_scale.dtype != torch.float32:
+            raise ValueError("mx_matvec: tensor_scale must be fp32")
+        ts = _buffer(w.tensor_scale, 4, dev, "mx_matvec", "tensor_scale")
+    q = _PACK_QTENSOR(_buffer(w.codes, held // 2, dev, "mx_matvec", "codes"), _buffer(w.scales, blocks, dev, "mx_matvec", "scales"),
+                      offsets, macro, ts, 0, n, k)
     _check(lib().mx_matvec(f, q, _code(x.dtype), x.data_ptr(), tokens, ldx, bp, y.data_ptr(), ldy, _code(y.dtype),
                            _stream_ptr(dev, "mx_matvec")), "mx_matvec")
     return y

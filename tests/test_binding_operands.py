@@ -137,3 +137,42 @@ def test_workspace_bytes(machine):
     """A workspace of any type counts by its bytes."""
     attend(workspace=zeros(1 << 20, dtype=torch.float32))
     assert 4 << 20 in machine.launches[0][1]
+
+
+@pytest.mark.parametrize("kind", WEIGHTS)
+def test_weight_buffers_too_small(machine, kind):
+    """One byte (or value) less than rows, columns and format need, each buffer in turn."""
+    fmt, sizes = WEIGHTS[kind]
+    x = zeros(3, 128)
+    for name, n in sizes.items():
+        dtype = KIND.get(name, torch.uint8)
+        mx.mx_matvec(fmt, weight(kind, **{name: zeros(n + 5, dtype=dtype)})[1], x)       # more than enough
+        machine.launches.clear()
+        with pytest.raises(ValueError, match=name):
+            mx.mx_matvec(fmt, weight(kind, **{name: zeros(n - 1, dtype=dtype)})[1], x)
+        assert not machine.launches, name
+
+
+def test_tensor_scale_of_another_type(machine):
+    fmt, w = weight("nvfp4", tensor_scale=zeros(2, dtype=torch.float64))
+    with pytest.raises(ValueError, match="tensor_scale"):
+        mx.mx_matvec(fmt, w, zeros(3, 128))
+    assert not machine.launches
+
+
+@pytest.mark.parametrize("fmt", [mx.MXFP8_E4M3, mx.Format(block_rows=32, block_cols=32), mx.Format(block_cols=0),
+                                 mx.Format(block_cols=24), mx.Format(elem=mx.ELEM_INT4, asymmetric=1)])
+def test_formats_and_missing_buffers_stay_the_library_s_to_refuse(fmt):
+    """The real library: formats without a kernel, and an absent buffer."""
+    import ctypes
+    u8 = torch.zeros(4096, dtype=torch.uint8)
+    f, q = fmt.c(), mx.QTensor(32, 128, u8, u8).c()
+    rc = mx.lib().mx_matvec(ctypes.byref(f), ctypes.byref(q), 1, u8.data_ptr(), 1, 128, None, u8.data_ptr(), 32, 1, None)
+    assert rc in (mx.MX_ERR_UNSUPPORTED, mx.MX_ERR_ARG)
+
+
+@pytest.mark.parametrize("fmt", [mx.MXFP8_E4M3, mx.Format(block_rows=32, block_cols=32), mx.Format(block_cols=0)])
+def test_formats_without_a_kernel_reach_the_library(machine, fmt):
+    w = mx.QTensor(32, 128, zeros(16, dtype=torch.uint8), zeros(1, dtype=torch.uint8))
+    mx.mx_matvec(fmt, w, zeros(3, 128))
+    assert len(machine.launches) == 1
