@@ -442,10 +442,13 @@ def _code(dtype):
 
 
 def _stream_ptr(dev, where):
-    """The stream of a launch whose operands lie on device `dev`."""
+    """The current stream, for a launch whose operands lie on device `dev`:
+    kernels run on the current device."""
     if dev < 0:
         raise ValueError(f"{where}: the operands must be GPU tensors")
-    return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+    if dev != torch._C._cuda_getDevice():
+        raise ValueError(f"{where}: the operands lie on device {dev}, the call (or its stream) runs on {torch._C._cuda_getDevice()}")
+    return torch._C._cuda_getCurrentRawStream(dev)
 
 
 def _raw(t):

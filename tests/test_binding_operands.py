@@ -176,3 +176,20 @@ def test_formats_without_a_kernel_reach_the_library(machine, fmt):
     w = mx.QTensor(32, 128, zeros(16, dtype=torch.uint8), zeros(1, dtype=torch.uint8))
     mx.mx_matvec(fmt, w, zeros(3, 128))
     assert len(machine.launches) == 1
+
+
+@pytest.mark.parametrize("call", CALLS)
+def test_another_gpu_than_the_current_one(machine, call):
+    """Operands of GPU 1 under a launch on GPU 0, by the current device and by
+    a stream of GPU 0; and on GPU 1 both ways."""
+    with pytest.raises(ValueError, match="device"):
+        call(card=1)
+    with pytest.raises(ValueError, match="device"):
+        call(card=1, stream=Stream(2, device=0))
+    with pytest.raises(ValueError, match="device"):
+        call(stream=Stream(7, device=1))
+    assert not machine.launches
+    call(card=1, stream=Stream(7, device=1))
+    machine.device = 1
+    call(card=1)
+    assert len(machine.launches) == 2
