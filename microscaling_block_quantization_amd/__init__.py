@@ -435,10 +435,10 @@ _PACK_ROPE = struct.Struct("@q4i4PqPf4x").pack
 
 
 def _code(dtype):
-    try:
-        return _DTYPES[dtype]
-    except KeyError:
-        raise TypeError(f"unsupported dtype {dtype}") from None
+    code = _DTYPES.get(dtype)
+    if code is None:
+        raise TypeError(f"unsupported dtype {dtype}")
+    return code
 
 
 def _stream_ptr(dev, where):
@@ -446,7 +446,7 @@ def _stream_ptr(dev, where):
     kernels run on the current device."""
     if dev < 0:
         raise ValueError(f"{where}: the operands must be GPU tensors")
-    if dev != torch._C._cuda_getDevice():
+    if torch._C._cuda_getDevice() != dev:
         raise ValueError(f"{where}: the operands lie on device {dev}, the call (or its stream) runs on {torch._C._cuda_getDevice()}")
     return torch._C._cuda_getCurrentRawStream(dev)
 
@@ -471,17 +471,10 @@ def _vector(t, n, dtype, dev, where, name):
 
 
 def _buffer(t, nbytes, dev, where, name):
-    """The address of a caller's buffer of at least nbytes (0: none)."""
-    if t is None:
-        return 0
+    """The address of a caller's buffer of at least nbytes."""
     if t.nbytes < nbytes or t.get_device() != dev or not t.is_contiguous():
         raise ValueError(f"{where}: {name} must be {nbytes} contiguous bytes at least, on the inputs' device")
     return t.data_ptr()
-
-
-def _workspace(t, dev, where):
-    """The address and bytes of a workspace."""
-    return _buffer(t, 0, dev, where, "workspace"), 0 if t is None else t.nbytes
 
 
 def mx_matvec(fmt: Format, w: QTensor, x: torch.Tensor, bias=None, y=None, out_dtype=None, stream=None):
@@ -491,39 +484,44 @@ def mx_matvec(fmt: Format, w: QTensor, x: torch.Tensor, bias=None, y=None, out_d
     tokens x N view to write into, else a new tensor of out_dtype (default: x's)."""
     if stream is not None:
         return _on(stream, mx_matvec, fmt, w, x, bias, y, out_dtype)
-    n, k = w.rows, w.cols
-    if x.dim() != 2 or x.size(1) != k or x.get_device() != w.codes.get_device():
+    n, k, codes, scales, dev, shape = w.rows, w.cols, w.codes, w.scales, x.get_device(), x.shape
+    if len(shape) != 2 or shape[1] != k or codes.get_device() != dev:
         raise ValueError(f"mx_matvec: x must be tokens x {k} on the weight's device")
-    tokens, dev = x.size(0), x.get_device()
+    tokens = shape[0]
     ldx, last = x.stride()
     if last != 1 and k > 1 and tokens:
         raise ValueError("mx_matvec: the rows of x must be contiguous")
     bp = 0 if bias is None else _vector(bias, n, x.dtype, dev, "mx_matvec", "bias")
     if y is None:
-        y = x.new_empty((tokens, n)) if out_dtype is None else x.new_empty((tokens, n), dtype=out_dtype)
+        y = x.new_empty((tokens, n)) if out_dtype is None or out_dtype is x.dtype else x.new_empty((tokens, n), dtype=out_dtype)
         ldy = n
     else:
-        if y.dim() != 2 or y.size(0) != tokens or y.size(1) != n or (y.stride(1) != 1 and n > 1 and tokens) or y.get_device() != dev:
+        if y.shape != (tokens, n) or (y.stride(1) != 1 and n > 1 and tokens) or y.get_device() != dev:
             raise ValueError(f"mx_matvec: y must be {tokens} x {n} with contiguous rows")
         ldy = y.stride(0)
     if tokens <= 1:
         ldx, ldy = k, n
-    f = _PACK_FORMAT(fmt.elem, fmt.scale, fmt.rule, fmt.round, fmt.block_rows, fmt.block_cols, fmt.asymmetric, fmt.hadamard,
-                     fmt.macro_cols, fmt.oas_tau, fmt.seed, fmt.rng_offset)
     # row blocks of 4-bit codes: any other format is the library's to refuse
-    held = n * k if fmt.block_rows == 1 and fmt.block_cols > 0 and fmt.elem in (ELEM_E2M1, ELEM_INT4) else 0
-    blocks = held // (fmt.block_cols or 1)
-    offsets = macro = ts = 0
-    if w.offsets is not None:
-        offsets = _buffer(w.offsets, 2 * blocks if fmt.asymmetric else 0, dev, "mx_matvec", "offsets")
-    if w.macro_scales is not None:
-        macro = _buffer(w.macro_scales, held // 128 if fmt.macro_cols else 0, dev, "mx_matvec", "macro_scales")
-    if w.tensor_scale is not None:
-        if w.tensor_scale.dtype != torch.float32:
+    bc, asym, offsets, macro, ts = fmt.block_cols, fmt.asymmetric, w.offsets, w.macro_scales, w.tensor_scale
+    held = n * k if bc > 0 and fmt.block_rows == 1 and fmt.elem in (ELEM_E2M1, ELEM_INT4) else 0
+    blocks = held // (bc or 1)
+    if (codes.nbytes < held // 2 or scales.nbytes < blocks or scales.get_device() != dev or not codes.is_contiguous() or
+            not scales.is_contiguous()):
+        _buffer(codes, held // 2, dev, "mx_matvec", "codes")
+        _buffer(scales, blocks, dev, "mx_matvec", "scales")
+    if offsets is not None:
+        if offsets.get_device() != dev or not offsets.is_contiguous() or (asym and offsets.nbytes < 2 * blocks):
+            _buffer(offsets, 2 * blocks if asym else 0, dev, "mx_matvec", "offsets")
+        offsets = offsets.data_ptr()
+    if macro is not None:
+        macro = _buffer(macro, held // 128 if fmt.macro_cols else 0, dev, "mx_matvec", "macro_scales")
+    if ts is not None:
+        if ts.dtype is not torch.float32:
             raise ValueError("mx_matvec: tensor_scale must be fp32")
-        ts = _buffer(w.tensor_scale, 4, dev, "mx_matvec", "tensor_scale")
-    q = _PACK_QTENSOR(_buffer(w.codes, held // 2, dev, "mx_matvec", "codes"), _buffer(w.scales, blocks, dev, "mx_matvec", "scales"),
-                      offsets, macro, ts, 0, n, k)
+        ts = _buffer(ts, 4, dev, "mx_matvec", "tensor_scale")
+    f = _PACK_FORMAT(fmt.elem, fmt.scale, fmt.rule, fmt.round, fmt.block_rows, bc, asym, fmt.hadamard, fmt.macro_cols, fmt.oas_tau,
+                     fmt.seed, fmt.rng_offset)
+    q = _PACK_QTENSOR(codes.data_ptr(), scales.data_ptr(), offsets or 0, macro or 0, ts or 0, 0, n, k)
     _check(lib().mx_matvec(f, q, _code(x.dtype), x.data_ptr(), tokens, ldx, bp, y.data_ptr(), ldy, _code(y.dtype),
                            _stream_ptr(dev, "mx_matvec")), "mx_matvec")
     return y
@@ -616,11 +614,13 @@ def mx_qk_rope_backward(dy_q, dy_k, q, k, cos, sin, positions, q_weight=None, k_
         dk, ok = _out_heads(dk, k, dim, dev, "mx_qk_rope_backward: dk")
     dqw = None if q_weight is None else cos.new_empty((dim,))
     dkw = None if k_weight is None else cos.new_empty((dim,))
-    if workspace is None and (dqw is not None or dkw is not None):
+    if workspace is not None:
+        _buffer(workspace, 0, dev, "mx_qk_rope_backward", "workspace")
+    elif dqw is not None or dkw is not None:
         workspace = cos.new_empty((lib().mx_qk_rope_workspace_size(r),), dtype=torch.uint8)
-    ws, nbytes = _workspace(workspace, dev, "mx_qk_rope_backward")
-    _check(lib().mx_qk_rope_backward(r, gq, gk, xq, xk, oq, ok, _raw(dqw), _raw(dkw), ws, nbytes,
-                                     _stream_ptr(dev, "mx_qk_rope_backward")), "mx_qk_rope_backward")
+    _check(lib().mx_qk_rope_backward(r, gq, gk, xq, xk, oq, ok, _raw(dqw), _raw(dkw), _raw(workspace),
+                                     0 if workspace is None else workspace.nbytes, _stream_ptr(dev, "mx_qk_rope_backward")),
+           "mx_qk_rope_backward")
     return dq, dk, dqw, dkw
 
 
@@ -729,8 +729,9 @@ def mx_attend(q, cache: KVCache, page_table, lengths, scale=None, out=None, lse=
         raise ValueError(f"mx_attend: lse must be a contiguous fp32 {batch} x {heads}")
     if workspace is None:
         workspace = cache.k.new_empty((lib().mx_attend_workspace_size(cache._ref, batch, heads, cols),), dtype=torch.uint8)
-    ws, nbytes = _workspace(workspace, dev, "mx_attend")
+    elif workspace.get_device() != dev or not workspace.is_contiguous():
+        _buffer(workspace, 0, dev, "mx_attend", "workspace")
     _check(lib().mx_attend(cache._ref, hq, batch, page_table.data_ptr(), cols, cols if batch <= 1 else stride, n,
-                           dim ** -0.5 if scale is None else scale, ho, _raw(lse), ws, nbytes,
+                           dim ** -0.5 if scale is None else scale, ho, _raw(lse), workspace.data_ptr(), workspace.nbytes,
                            _stream_ptr(dev, "mx_attend")), "mx_attend")
     return out if lse is None else (out, lse)
