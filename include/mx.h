@@ -422,7 +422,10 @@ int mx_cache_write(const mx_kv_cache *cache, const mx_heads *k, const mx_heads *
  *  - The length is split over workgroups, their parts joined in a fixed order;
  *    the same inputs give the same bits.  workspace: at least
  *    mx_attend_workspace_size bytes; no initial contents needed; calls that
- *    share one must not overlap.  table_cols * page_size < 2^30.             */
+ *    share one must not overlap.  That size serves every call of at most this
+ *    batch and these table_cols over a cache of the same format, page size,
+ *    heads and dim, with the same query heads: a server allocates it once for
+ *    its largest.  table_cols * page_size < 2^30.                            */
 size_t mx_attend_workspace_size(const mx_kv_cache *cache, int64_t batch, int32_t q_heads, int64_t table_cols);
 int mx_attend(const mx_kv_cache *cache, const mx_heads *q, int64_t batch, const int32_t *page_table,
               int64_t table_cols, int64_t table_stride, const int32_t *lengths, float scale,

@@ -694,10 +694,13 @@ def mx_cache_write(cache: KVCache, k, v, slots, stream=None):
 
 
 def mx_attend_workspace_size(cache: KVCache, batch, q_heads, table_cols):
+    """Workspace bytes of mx_attend for at most `batch` sequences of at most
+    `table_cols` pages."""
     return int(lib().mx_attend_workspace_size(cache._ref, batch, q_heads, table_cols))
 
 
 def alloc_attend_workspace(cache: KVCache, batch, q_heads, table_cols):
+    """A workspace for calls of at most `batch` sequences of at most `table_cols` pages."""
     return _empty(mx_attend_workspace_size(cache, batch, q_heads, table_cols), cache.k.device)
 
 

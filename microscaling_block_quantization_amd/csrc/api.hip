@@ -340,9 +340,9 @@ int check_attend(const mx_kv_cache* c, int64_t batch, int32_t q_heads, int64_t c
     return MX_OK;
 }
 
-size_t attend_bytes(const mx_kv_cache* c, int64_t batch, int32_t q_heads, int64_t cols) {
-    const int64_t workers = mxk::attend_plan(cache_params(c), batch, q_heads, cols).workers;
-    return workers && batch ? round_up((size_t)q_heads * (workers + batch) * (c->dim + 2) * sizeof(float)) : 0;
+// the workspace of a call whose query heads have this many slots each
+size_t attend_bytes(const mx_kv_cache* c, int32_t q_heads, int64_t slots) {
+    return round_up((size_t)q_heads * slots * (c->dim + 2) * sizeof(float));
 }
 
 }  // namespace
@@ -758,7 +758,7 @@ int mx_cache_write(const mx_kv_cache* cache, const mx_heads* k, const mx_heads* 
 
 size_t mx_attend_workspace_size(const mx_kv_cache* cache, int64_t batch, int32_t q_heads, int64_t table_cols) {
     if (check_cache(cache, false) || check_attend(cache, batch, q_heads, table_cols)) return 0;
-    return attend_bytes(cache, batch, q_heads, table_cols);
+    return attend_bytes(cache, q_heads, mxk::attend_slots(cache_params(cache), batch, q_heads, table_cols));
 }
 
 int mx_attend(const mx_kv_cache* cache, const mx_heads* q, int64_t batch, const int32_t* page_table, int64_t table_cols,
@@ -777,7 +777,8 @@ int mx_attend(const mx_kv_cache* cache, const mx_heads* q, int64_t batch, const 
     if (rc) return rc;
     if (!lengths || (table_cols && !page_table) || (batch > 1 && table_stride < table_cols)) return MX_ERR_ARG;
     if (!aligned_to(lse, 4) || !aligned_to(lengths, 4) || !aligned_to(page_table, 4)) return MX_ERR_ALIGN;
-    const size_t need = attend_bytes(cache, batch, q->heads, table_cols);
+    const mxk::AttendPlan a = mxk::attend_plan(cache_params(cache), batch, q->heads, table_cols);
+    const size_t need = a.workers ? attend_bytes(cache, q->heads, a.workers + batch) : 0;
     if (need && (!workspace || ws_bytes < need)) return MX_ERR_WORKSPACE;
     if (need && !aligned16(workspace)) return MX_ERR_ALIGN;
     mxk::AttendParams p;
@@ -798,7 +799,6 @@ int mx_attend(const mx_kv_cache* cache, const mx_heads* q, int64_t batch, const 
     p.scale = scale;
     p.lse = lse;
     p.parts = static_cast<float*>(workspace);
-    const mxk::AttendPlan a = mxk::attend_plan(p.c, batch, q->heads, table_cols);
     p.waves = a.waves;
     p.workers = a.workers;
     return hip_status(mxk::launch_attend(p, q->dtype == MX_DTYPE_BF16, static_cast<hipStream_t>(stream)));

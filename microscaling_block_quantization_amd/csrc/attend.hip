@@ -826,6 +826,10 @@ hipError_t launch_cache_write(CacheWrite p, bool bf, hipStream_t s) {
 
 bool attend_dim_ok(int d) { return d == 64 || d == 96 || d == 128 || d == 192 || d == 256; }
 
+// pairs of a key-value head and 16 of its query heads
+static int64_t planes_of(const KvCache& c, int q_heads) { return (int64_t)c.heads * ((q_heads / c.heads + QH - 1) / QH); }
+constexpr int64_t FULL = 256;          // whole sequences that fill the chip, one for each CU
+
 // How a call is split.  Short sequences (one tile a wave, or four if there are
 // enough of them to fill the chip): eight waves take a whole one and no join
 // follows (32 sequences of 777: 17 us, shared out 25; one of 777: 12 us, shared
@@ -835,14 +839,25 @@ bool attend_dim_ok(int d) { return d == 64 || d == 96 || d == 128 || d == 192 ||
 // to 8192 tokens of 128 values: bf16 106 and 120, MXFP8 84 and 68, MXFP4 71 and
 // 52; bf16 of 64 values, half the tokens: 44 and 37).
 AttendPlan attend_plan(const KvCache& c, int64_t batch, int q_heads, int64_t cols) {
-    const int group = q_heads / c.heads;
-    const int64_t planes = (int64_t)c.heads * ((group + QH - 1) / QH), longest = cols * c.page;
-    if (c.dim <= EIGHT_MAX && (longest <= 8 * TILE || (longest <= 8 * TILE * 4 && batch * planes >= 256))) return AttendPlan{8, 0};
+    const int64_t planes = planes_of(c, q_heads), longest = cols * c.page;
+    if (c.dim <= EIGHT_MAX && (longest <= 8 * TILE || (longest <= 8 * TILE * 4 && batch * planes >= FULL))) return AttendPlan{8, 0};
     const int64_t want = c.dim * kind_bits(c.kind) / 8 >= 256 ? 256 : 768;
     int64_t workers = (want + planes - 1) / planes;
     const int64_t most = batch * ((longest + UNIT - 1) / UNIT);
     if (workers > most) workers = most;
     return AttendPlan{4, (int)(workers < 1 ? 1 : workers)};
+}
+
+// Workers and slots grow with batch and columns, but for one step: a batch that
+// fills the chip with whole sequences needs none where a smaller one does.
+int64_t attend_slots(const KvCache& c, int64_t batch, int q_heads, int64_t cols) {
+    AttendPlan a = attend_plan(c, batch, q_heads, cols);
+    if (!a.workers) {
+        const int64_t most = (FULL - 1) / planes_of(c, q_heads);
+        if (batch > most) batch = most;
+        a = attend_plan(c, batch, q_heads, cols);
+    }
+    return a.workers && batch ? a.workers + batch : 0;
 }
 
 hipError_t launch_attend(AttendParams p, bool bf, hipStream_t s) {

@@ -96,6 +96,9 @@ struct AttendPlan {
     int waves, workers;
 };
 AttendPlan attend_plan(const KvCache& c, int64_t batch, int q_heads, int64_t cols);
+// Most slots per query head (workers + sequences, 0 without workers) of any call
+// of at most this batch and these columns
+int64_t attend_slots(const KvCache& c, int64_t batch, int q_heads, int64_t cols);
 bool attend_dim_ok(int dim);
 hipError_t launch_attend(AttendParams p, bool q_bf16, hipStream_t s);
 
