@@ -303,7 +303,11 @@ int mx_gemm(const mx_format *fa, const mx_qtensor *a, const mx_format *fb,
  * gradient, for training), the write of new keys and values to a paged cache,
  * and the attention of one new token per sequence over that cache.  Index
  * vectors (positions, slots, lengths, page numbers) and lse need the alignment
- * of their elements alone, so slices of them serve.                          */
+ * of their elements alone, so slices of them serve.  A call whose launch would
+ * hold 2^32 threads or more is refused (MX_ERR_ARG, nothing launched): none is
+ * with up to 2^28 - 32 weight rows, 2^26 - 256 head vectors of mx_qk_rope,
+ * 2^27 - 8 of mx_cache_write, and fewer than 2^23 pairs of a sequence and a
+ * query head of mx_attend; larger calls are where their lanes do more each.  */
 
 /* y = x . deq(W)^T + bias for a few tokens: x is tokens x w->cols (row stride
  * ldx elements, dtype x_dtype), W a quantized tensor of w->rows x w->cols, y
@@ -321,7 +325,8 @@ int mx_gemm(const mx_format *fa, const mx_qtensor *a, const mx_format *fb,
  *  - A NaN scale code makes its row's outputs NaN, a NaN or Inf in a token
  *    makes that token's outputs non-finite, other tokens are untouched.
  *  - Any number of tokens runs; the kernel is made for up to 16 (more read the
- *    weight once per 16).  w->rows < 2^31, 0 < w->cols < 2^24, tokens <= 1048560.
+ *    weight once per 16).  0 < w->cols < 2^24, tokens <= 1048560, w->rows < 2^31
+ *    and no more than a launch holds (above).
  *  - x, W's buffers, bias and y 16-byte aligned, ldx a multiple of 16 bytes
  *    (MX_ERR_ALIGN).  y must not overlap an input.                           */
 int mx_matvec(const mx_format *fw, const mx_qtensor *w, int x_dtype, const void *x, int64_t tokens,
@@ -345,7 +350,8 @@ typedef struct mx_heads {
  * with (a, b) = (i, i + rot_dim/2), or (2i, 2i + 1) when `interleaved`, and
  * cos, sin at [p][i] of two tables of table_rows x rot_dim/2 fp32 values.  A
  * position outside the table makes that token's rotated values NaN (all of
- * its gradients through a norm).  tokens x heads < 2^31.  Everything
+ * its gradients through a norm).  tokens x heads < 2^31, and no more than a
+ * launch holds (above).  Everything
  * between load and store is fp32.  q_weight and k_weight have w_dtype.       */
 typedef struct mx_rope {
     int64_t tokens;
@@ -399,7 +405,8 @@ typedef struct mx_kv_cache {
  * page slots[i] / page_size at slots[i] % page_size; a slot outside the cache
  * (negative, or past its end) skips the token.  Codes and scales are those
  * mx_quantize writes for the same values.  Two tokens of one slot in one call
- * leave either's values.  tokens x heads < 2^30.                             */
+ * leave either's values.  tokens x heads < 2^30, and no more than a launch
+ * holds (above).                                                             */
 int mx_cache_write(const mx_kv_cache *cache, const mx_heads *k, const mx_heads *v, int64_t tokens,
                    const int64_t *slots, void *stream);
 

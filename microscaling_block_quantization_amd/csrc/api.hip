@@ -251,6 +251,8 @@ int static_scratch(uint8_t** ptr) {
     return MX_OK;
 }
 
+int launch_status(hipError_t e) { return e == mxk::TOO_LARGE ? MX_ERR_ARG : hip_status(e); }
+
 // ---- checks of the decode-step entry points --------------------------------
 // index vectors (positions, slots, lengths, page numbers) may be slices
 bool aligned_to(const void* p, uintptr_t n) { return ((uintptr_t)p & (n - 1)) == 0; }
@@ -646,7 +648,7 @@ int mx_matvec(const mx_format* fw, const mx_qtensor* w, int x_dtype, const void*
     p.y = y;
     p.ldy = ldy;
     p.y_bf16 = y_dtype == MX_DTYPE_BF16;
-    return hip_status(mxk::launch_matvec(p, static_cast<hipStream_t>(stream)));
+    return launch_status(mxk::launch_matvec(p, static_cast<hipStream_t>(stream)));
 }
 
 int mx_qk_rope(const mx_rope* r, const mx_heads* q, const mx_heads* k, const mx_heads* q_out, const mx_heads* k_out,
@@ -677,7 +679,7 @@ int mx_qk_rope(const mx_rope* r, const mx_heads* q, const mx_heads* k, const mx_
     }
     if (!k) p.set[1].w = nullptr;
     if (r->tokens >= ((int64_t)1 << 31) / heads) return MX_ERR_ARG;
-    return hip_status(mxk::launch_rope(p, q->dtype == MX_DTYPE_BF16, false, static_cast<hipStream_t>(stream)));
+    return launch_status(mxk::launch_rope(p, q->dtype == MX_DTYPE_BF16, false, static_cast<hipStream_t>(stream)));
 }
 
 size_t mx_qk_rope_workspace_size(const mx_rope* r) {
@@ -724,7 +726,7 @@ int mx_qk_rope_backward(const mx_rope* r, const mx_heads* dy_q, const mx_heads* 
     p.set[0].dw = dq_weight;
     p.set[1].dw = dk_weight;
     p.set[0].parts = static_cast<float*>(workspace);
-    return hip_status(mxk::launch_rope(p, q->dtype == MX_DTYPE_BF16, true, static_cast<hipStream_t>(stream)));
+    return launch_status(mxk::launch_rope(p, q->dtype == MX_DTYPE_BF16, true, static_cast<hipStream_t>(stream)));
 }
 
 int mx_cache_write(const mx_kv_cache* cache, const mx_heads* k, const mx_heads* v, int64_t tokens, const int64_t* slots,
@@ -753,7 +755,7 @@ int mx_cache_write(const mx_kv_cache* cache, const mx_heads* k, const mx_heads* 
     p.tokens = tokens;
     p.rule = cache->format ? cache->format->rule : 0;
     p.tau = cache->format ? cache->format->oas_tau : 0.0f;
-    return hip_status(mxk::launch_cache_write(p, k->dtype == MX_DTYPE_BF16, static_cast<hipStream_t>(stream)));
+    return launch_status(mxk::launch_cache_write(p, k->dtype == MX_DTYPE_BF16, static_cast<hipStream_t>(stream)));
 }
 
 size_t mx_attend_workspace_size(const mx_kv_cache* cache, int64_t batch, int32_t q_heads, int64_t table_cols) {
@@ -801,7 +803,7 @@ int mx_attend(const mx_kv_cache* cache, const mx_heads* q, int64_t batch, const 
     p.parts = static_cast<float*>(workspace);
     p.waves = a.waves;
     p.workers = a.workers;
-    return hip_status(mxk::launch_attend(p, q->dtype == MX_DTYPE_BF16, static_cast<hipStream_t>(stream)));
+    return launch_status(mxk::launch_attend(p, q->dtype == MX_DTYPE_BF16, static_cast<hipStream_t>(stream)));
 }
 
 }  // extern "C"

@@ -768,6 +768,8 @@ template <int D, int KIND, bool QF32, bool PAGE16, int AW>
 hipError_t go(const AttendParams& p, hipStream_t s) {
     const int group = p.q_heads / p.c.heads, tiles = (group + QH - 1) / QH, rows = group < QH ? group : QH;
     const int64_t n = p.c.heads * tiles * (p.workers ? p.workers : p.batch);
+    const int64_t joins = p.workers ? p.batch * p.q_heads : 0;
+    if (!grid_ok(n, 64 * AW) || !grid_ok(joins, 256)) return TOO_LARGE;
     const int lds = AW * rows * (D + 3) * (int)sizeof(float);
     if (lds > 64 * 1024) {
         const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(k_attend<D, KIND, QF32, PAGE16, AW>),
@@ -776,8 +778,8 @@ hipError_t go(const AttendParams& p, hipStream_t s) {
     }
     k_attend<D, KIND, QF32, PAGE16, AW><<<(unsigned)n, 64 * AW, lds, s>>>(p);
     hipError_t e = hipGetLastError();
-    if (e != hipSuccess || !p.workers) return e;
-    k_attend_join<D, QF32><<<(unsigned)(p.batch * p.q_heads), 256, 0, s>>>(p);
+    if (e != hipSuccess || !joins) return e;
+    k_attend_join<D, QF32><<<(unsigned)joins, 256, 0, s>>>(p);
     return hipGetLastError();
 }
 
@@ -797,6 +799,7 @@ template <int D, int KIND>
 hipError_t write_as(const CacheWrite& p, bool bf, hipStream_t s) {
     constexpr int PER = CT / (D / 8);
     const int64_t n = p.tokens * p.c.heads;
+    if (!grid_ok((n + PER - 1) / PER, CT)) return TOO_LARGE;
     const unsigned grid = (unsigned)((n + PER - 1) / PER);
     if (bf) k_cache_write<D, KIND, true><<<grid, CT, 0, s>>>(p);
     else k_cache_write<D, KIND, false><<<grid, CT, 0, s>>>(p);

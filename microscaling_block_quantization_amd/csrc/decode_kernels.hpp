@@ -7,6 +7,11 @@
 
 namespace mxk {
 
+// HIP takes fewer than 2^32 threads along a grid's axis.  A launcher returns
+// this, with nothing launched, where a call would need more.
+constexpr hipError_t TOO_LARGE = hipErrorInvalidConfiguration;
+inline bool grid_ok(int64_t blocks, int threads) { return blocks * threads < (int64_t)1 << 32; }
+
 struct MatvecParams {
     const uint8_t* codes;          // n x k/2
     const uint8_t* scales;         // n x k / block

@@ -610,7 +610,9 @@ ScaleDec scale_dec(int scale) {
 
 template <bool INT, bool MUL, bool OFF, int BK, int XP, int RT>
 hipError_t go_short(const MatvecParams& p, hipStream_t s) {
-    const dim3 grid((unsigned)((p.n + 16 * RT - 1) / (16 * RT)), (unsigned)((p.tokens + TOK - 1) / TOK));
+    const int64_t n = (p.n + 16 * RT - 1) / (16 * RT);
+    if (!grid_ok(n, 512)) return TOO_LARGE;
+    const dim3 grid((unsigned)n, (unsigned)((p.tokens + TOK - 1) / TOK));
     k_short<INT, MUL, OFF, BK, XP, RT><<<grid, 512, 0, s>>>(p, scale_dec(p.scale));
     return hipGetLastError();
 }
@@ -621,6 +623,7 @@ hipError_t go_tall(const MatvecParams& p, hipStream_t s) {
     const int64_t all = (p.n + 15) / 16;
     int64_t tiles = (all + 255) / 256;
     if (tiles > TALL_TILES) tiles = TALL_TILES;
+    if (!grid_ok((all + tiles - 1) / tiles, 64 * KW)) return TOO_LARGE;
     const dim3 grid((unsigned)((all + tiles - 1) / tiles), (unsigned)((p.tokens + TOK - 1) / TOK));
     k_tall<INT, MUL, OFF, BK, XP><<<grid, 64 * KW, (int)tiles * KW * 1024, s>>>(p, scale_dec(p.scale), (int)tiles);
     return hipGetLastError();

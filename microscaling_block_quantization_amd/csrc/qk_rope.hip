@@ -546,6 +546,7 @@ template <bool BF, int LP, int HB>
 hipError_t forward(RopeParams& p, hipStream_t s) {
     const uint32_t n = set_blocks(p, LP, HB, 0);
     if (!n) return hipSuccess;
+    if (!grid_ok(n, RT)) return TOO_LARGE;
     if (streams(p, BF)) k_rope<BF, LP, HB, true><<<n, RT, 0, s>>>(p);
     else k_rope<BF, LP, HB, false><<<n, RT, 0, s>>>(p);
     return hipGetLastError();
