@@ -319,9 +319,13 @@ int mx_gemm(const mx_format *fa, const mx_qtensor *a, const mx_format *fb,
  *    matter.  Anything else (other elements, E3M0 scales, rotation, column or
  *    2D blocks): MX_ERR_UNSUPPORTED.
  *  - W's values enter exactly (decoded to bf16, which holds every code times
- *    its scale, down to bf16's own smallest values), an fp32 x as the exact
- *    sum of three bf16 parts; products are summed in fp32 in a fixed order.
- *    An offset or the INT4 bias enters as offset times the block's sum of x.
+ *    its scale as multiples of 2^-133; INT4 as multiples of 2^-129, which only
+ *    macro scales can need more of), an fp32 x as the exact sum of three bf16
+ *    parts (multiples of 2^-133); products are summed in fp32 in a fixed order.
+ *    An offset or the INT4 bias enters as offset times the block's sum of x
+ *    (multiples of 2^-129 beside INT4 offsets).  Symmetric INT4 is (u - 8) s
+ *    with u = 0 .. 15, summed as u s x and -8 s x: its sums round by |u s x| and
+ *    |8 s x|.
  *  - A NaN scale code makes its row's outputs NaN, a NaN or Inf in a token
  *    makes that token's outputs non-finite, other tokens are untouched.
  *  - Any number of tokens runs; the kernel is made for up to 16 (more read the

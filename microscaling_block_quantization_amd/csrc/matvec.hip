@@ -2,14 +2,17 @@
 // a 4-bit weight W in row blocks.
 //
 // Mathematics.  A weight is q s (+ o): the code's value q, its block's scale s
-// and, for asymmetric blocks, an offset o.  q s is exact in bf16: E2M1 has two
+// and, for asymmetric blocks, an offset o.  q s is exact in bf16 (down to its
+// smallest step, 2^-133; 2^-129 for INT4, see decode8w): E2M1 has two
 // significant bits, a scale at most four, an INT4 code u = 0 .. 15 four.  INT4
 // is taken as u with an offset (the min/max offset, or -8 s for a symmetric
 // two's complement nibble, whose u is the nibble with its top bit flipped), and
 // sum_k (q s + o) x = sum_k (q s) x + sum_blocks o X, X the block's sum of x.
 // The second sum runs on the same matrix instruction, one K position per bf16
 // part of X (three parts hold all 24 bits) and block.  An fp32 x is the exact
-// sum of three bf16 parts, one product each.
+// sum of three bf16 parts, one product each (what of it lies below 2^-133 is
+// not: parts are bf16 numbers).  A symmetric INT4 block's terms are u s x and
+// -8 s X, so its rounding goes by those and not by q s x.
 //
 // The 16 x 16 x 32 bf16 instruction takes W as its 16 rows and x as its 16
 // columns: for fewer tokens the other columns repeat the last token and are
@@ -92,17 +95,21 @@ __device__ __forceinline__ bf2v mul2(f2v q, float s) {
 
 // The eight codes of w times their scale as bf16.  INT4 codes are spread to
 // bytes (even codes, then odd ones: x is staged in that order) and go through
-// the FP8 converter: the E4M3 code u = 0 .. 15 stands for u 2^-9, so INT4
-// results are 2^-9 too small; the caller multiplies its sums by 2^9.
+// the FP8 converter: the E4M3 code u = 0 .. 15 stands for u 2^-9.  INT4 results
+// are held 2^-4 too small and the sums multiplied by 2^4 at the end: u s 2^-4
+// is exact in bf16 at the smallest E8M0 scale (2^-131 is four of its smallest
+// steps) and stays finite at the largest.  s here is what the converter takes,
+// 2^5 of the scale for INT4 without MUL.
+constexpr float INT_DOWN = 0x1p-4f, INT_CVT = 0x1p5f;
 template <bool INT, bool MUL>
 __device__ __forceinline__ bf8v decode8w(uint32_t w, float s) {
     if constexpr (INT) {
         const int lo = (int)(w & 0x0f0f0f0fu), hi = (int)((w >> 4) & 0x0f0f0f0fu);
         if constexpr (MUL) {
-            return join4(mul2(__builtin_amdgcn_cvt_scalef32_pk_f32_fp8(lo, 1.0f, false), s),
-                         mul2(__builtin_amdgcn_cvt_scalef32_pk_f32_fp8(lo, 1.0f, true), s),
-                         mul2(__builtin_amdgcn_cvt_scalef32_pk_f32_fp8(hi, 1.0f, false), s),
-                         mul2(__builtin_amdgcn_cvt_scalef32_pk_f32_fp8(hi, 1.0f, true), s));
+            return join4(mul2(__builtin_amdgcn_cvt_scalef32_pk_f32_fp8(lo, INT_CVT, false), s),
+                         mul2(__builtin_amdgcn_cvt_scalef32_pk_f32_fp8(lo, INT_CVT, true), s),
+                         mul2(__builtin_amdgcn_cvt_scalef32_pk_f32_fp8(hi, INT_CVT, false), s),
+                         mul2(__builtin_amdgcn_cvt_scalef32_pk_f32_fp8(hi, INT_CVT, true), s));
         } else {
             return join4(__builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, s, false),
                          __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, s, true),
@@ -147,9 +154,10 @@ struct Cols {
     bf8v b[4][XP];
     uint32_t sum[OFF ? scales_of(BK) : 1][2];
 };
-// v: the 32 values as loaded
+// v: the 32 values as loaded.  Beside INT4's given offsets, which enter as they
+// are, the sums carry the operands' 2^-4.
 template <bool INT, bool OFF, int BK, int XP>
-__device__ __forceinline__ void make_cols(Cols<OFF, BK, XP>& c, const u32x4 (&v)[4][XP == 1 ? 1 : 2]) {
+__device__ __forceinline__ void make_cols(Cols<OFF, BK, XP>& c, const u32x4 (&v)[4][XP == 1 ? 1 : 2], bool offsets) {
     constexpr int NSB = scales_of(BK);
     float X[NSB];
 #pragma unroll
@@ -193,7 +201,7 @@ __device__ __forceinline__ void make_cols(Cols<OFF, BK, XP>& c, const u32x4 (&v)
 #pragma unroll
         for (int b = 0; b < NSB; b++) {
             uint16_t h, m, l;
-            split3(X[b], h, m, l);
+            split3(INT && offsets ? X[b] * INT_DOWN : X[b], h, m, l);
             c.sum[b][0] = h | (uint32_t)m << 16;
             c.sum[b][1] = l;
         }
@@ -208,22 +216,41 @@ struct Side {
     uint32_t off[OFF ? scales_of(BK) : 1];
 };
 
-// acc += codes . x of one step
-template <bool INT, bool MUL, bool OFF, int BK, int XP>
+// Not 0 where a scale byte holds a code of 248 or more (its upper five bits are
+// all set): from code 250 on the converter's 2^5 s overflows, and INT4 codes go
+// through fp32.
+__device__ __forceinline__ uint32_t far_codes(uint32_t sc) {
+    const uint32_t low = ~sc & 0xf8f8f8f8u;
+    return (low - 0x01010101u) & ~low & 0x80808080u;
+}
+
+// acc += codes . x of one step.  far: whether a lane's step has such a scale,
+// or 2 to look; the seldom path (FAR) is kept from spreading over the other's
+// registers.
+template <bool INT, bool MUL, bool OFF, int BK, int XP, bool FAR = false>
 __device__ __forceinline__ void step_product(f4v& acc, u32x4 w, const Side<OFF, BK>& sd, const Cols<OFF, BK, XP>& x, ScaleDec dec,
-                                             bool macro, bool offsets) {
+                                             bool macro, bool offsets, int far = 2) {
     constexpr int NSB = scales_of(BK);
+    constexpr bool CVT = INT && !MUL;
+    if constexpr (CVT) {
+        const uint32_t low = ~sd.sc & 0xf8f8f8f8u;
+        if (far == 2 ? __any((low - 0x01010101u) & ~low & 0x80808080u) : far) {
+            // as other values, so that none of this is formed before the branch
+            Side<OFF, BK> d = sd;
+            asm volatile("" : "+v"(w), "+v"(d.sc));
+            step_product<INT, true, OFF, BK, XP, true>(acc, w, d, x, dec, false, offsets);
+            return;
+        }
+    }
     float s[NSB];
     uint32_t off[NSB];
 #pragma unroll
     for (int b = 0; b < NSB; b++) {
-        s[b] = mv_scale((sd.sc >> (8 * b)) & 0xffu, dec);
+        const uint32_t code = (sd.sc >> (8 * b)) & 0xffu;
+        s[b] = CVT ? bitsf((code + 5) << 23) : mv_scale(code, dec);      // CVT: 2^5 s, of code 0 too, and no NaN
         if (MUL && macro) s[b] *= mv_scale(sd.mac, ScaleDec{0x1p120f, 0x7fu});
-        if constexpr (OFF) {
-            // a power of two times a bf16: exact (INT4 sums are 2^-9 too small)
-            const float o = offsets ? bf16f((uint16_t)sd.off[b]) * (INT ? 0x1p-9f : 1.0f) : s[b] * -0x1p-6f;
-            off[b] = fbits(o) >> 16;
-        }
+        // -8 s 2^-4: a scale's four bits at most, exact in bf16
+        if constexpr (OFF) off[b] = offsets ? sd.off[b] : fbits(s[b] * (-8.0f * INT_DOWN / (CVT ? INT_CVT : 1.0f))) >> 16;
     }
 #pragma unroll
     for (int j = 0; j < 4; j++) {
@@ -231,6 +258,7 @@ __device__ __forceinline__ void step_product(f4v& acc, u32x4 w, const Side<OFF, 
         const bf8v a = decode8w<INT, MUL>(INT && !offsets ? c ^ 0x88888888u : c, s[j * NSB / 4]);
 #pragma unroll
         for (int part = 0; part < XP; part++) acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, x.b[j][part], acc, 0, 0, 0);
+        if (FAR) __builtin_amdgcn_sched_barrier(0);
     }
     if constexpr (OFF) {
         // o X: o in the first three of four K positions per sub-block
@@ -328,7 +356,7 @@ __device__ __forceinline__ const char* x_row(const MatvecParams& p, int64_t t0, 
 // what every sum is multiplied by
 template <bool INT>
 __device__ __forceinline__ float last_scale(const MatvecParams& p) {
-    return (p.tensor_scale ? *p.tensor_scale : 1.0f) * (INT ? 512.0f : 1.0f);
+    return (p.tensor_scale ? *p.tensor_scale : 1.0f) * (INT ? 1.0f / INT_DOWN : 1.0f);
 }
 // y of token t and row n from its sum
 template <bool INT, int XP>
@@ -346,9 +374,12 @@ __device__ __forceinline__ void put(const MatvecParams& p, int64_t t, int64_t n,
 // ---------------------------------------------------------------------------
 // Short K: each wave takes every eighth step of K for RT tiles of 16 rows, the
 // next step's codes, scales and x in registers while it multiplies this one's.
+// INT4 in blocks of 8 is held to 128 registers, four waves a SIMD, which puts 16
+// bytes of two tiles' state to memory (1 x 14336 x 4096 18.8 us, with 132
+// registers 20.0; 8 x 40000 x 1024 14.2 and 17.6).
 // ---------------------------------------------------------------------------
 template <bool INT, bool MUL, bool OFF, int BK, int XP, int RT>
-__global__ __launch_bounds__(512) void k_short(MatvecParams p, ScaleDec dec) {
+__global__ __launch_bounds__(512, INT && !MUL && BK == B_8 && XP == 1 ? 4 : 1) void k_short(MatvecParams p, ScaleDec dec) {
     constexpr int WAVES = 8, HOP = WAVES * STEP;
     __shared__ __attribute__((aligned(16))) float red[WAVES][RT][256];
     struct St {
@@ -380,7 +411,7 @@ __global__ __launch_bounds__(512) void k_short(MatvecParams p, ScaleDec dec) {
     for (int t = 0; t < RT; t++) acc[t] = f4v{0.f, 0.f, 0.f, 0.f};
     auto multiply = [&](const St& o) {
         Cols<OFF, BK, XP> c;
-        make_cols<INT>(c, o.x);
+        make_cols<INT>(c, o.x, offsets);
 #pragma unroll
         for (int t = 0; t < RT; t++) step_product<INT, MUL, OFF, BK, XP>(acc[t], o.w[t], o.d[t], c, dec, macro, offsets);
     };
@@ -546,11 +577,12 @@ __global__ __launch_bounds__(64 * KW, 2) void k_tall(MatvecParams p, ScaleDec de
                 Sd d[SS];
 #pragma unroll
                 for (int i = 0; i < SS; i++) side_of(d[i], f, i);
+                const int far = INT && !MUL ? __any(far_codes(f.sc[0]) | far_codes(f.sc[NSB - 1])) : 0;      // of all its steps
                 const int next = row_of(t + 1);
                 if constexpr (again.value) load_span(f, next, k0);
 #pragma unroll
                 for (int i = 0; i < SS; i++) {
-                    step_product<INT, MUL, OFF, BK, XP>(acc, w[i], d[i], c[i], dec, macro, offsets);
+                    step_product<INT, MUL, OFF, BK, XP>(acc, w[i], d[i], c[i], dec, macro, offsets, far);
                     if constexpr (again.value) w[i] = load_w(next, k0 + i * STEP);
                     MV_FENCE;
                 }
@@ -563,7 +595,7 @@ __global__ __launch_bounds__(64 * KW, 2) void k_tall(MatvecParams p, ScaleDec de
             for (int i = 0; i < SS; i++) w[i] = load_w(row_of(0), k0 + i * STEP);
             MV_FENCE;
 #pragma unroll
-            for (int i = 0; i < SS; i++) make_cols<INT>(c[i], xv[i]);
+            for (int i = 0; i < SS; i++) make_cols<INT>(c[i], xv[i], offsets);
             for (int t = 0; t + 1 < nt; t++) use(t, std::integral_constant<bool, true>{});
             use(nt - 1, std::integral_constant<bool, false>{});
         } else if (base == 0) {
@@ -577,7 +609,7 @@ __global__ __launch_bounds__(64 * KW, 2) void k_tall(MatvecParams p, ScaleDec de
         if (st < whole) load_x<XP>(xv, xrow, k0);
         else load_x_end<XP>(xv, xrow, k0, left);
         Cols<OFF, BK, XP> c;
-        make_cols<INT>(c, xv);
+        make_cols<INT>(c, xv, offsets);
         for (int t = 0; t < nt; t++) {
             u32x4 w;
             Sd d;
