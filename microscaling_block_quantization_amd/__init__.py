@@ -426,7 +426,8 @@ def mx_gemm(fa: Format, a: QTensor, fb: Format, b: QTensor, c=None, out_dtype=to
 # These kernels take a few microseconds, so the host's share of a call counts:
 # each check is one cheap comparison whose message is only formed when it
 # fails, and structs are packed as bytes.  `stream`: the stream to launch on
-# (default: the current one), see _on.
+# (default: the current one), see _on.  The calls record nothing for autograd
+# (mx_qk_rope_backward is the gradient to put into a Function).
 _DTYPES = {torch.float32: DTYPE_F32, torch.bfloat16: DTYPE_BF16}
 _PACK_FORMAT = struct.Struct("@9if2Q").pack
 _PACK_QTENSOR = struct.Struct("@6P2q").pack
@@ -453,6 +454,12 @@ def _stream_ptr(dev, where):
 
 def _raw(t):
     return 0 if t is None else t.data_ptr()
+
+
+def _changed(*ts):
+    """Tensors of the caller's that a launch writes into: autograd's count of
+    their changes goes up, as torch's own in-place operations do."""
+    torch._C._increment_version([t for t in ts if t is not None and not t.is_inference()])
 
 
 def _heads(t, dim, dev, what):
@@ -492,7 +499,8 @@ def mx_matvec(fmt: Format, w: QTensor, x: torch.Tensor, bias=None, y=None, out_d
     if last != 1 and k > 1 and tokens:
         raise ValueError("mx_matvec: the rows of x must be contiguous")
     bp = 0 if bias is None else _vector(bias, n, x.dtype, dev, "mx_matvec", "bias")
-    if y is None:
+    given = y is not None
+    if not given:
         y = x.new_empty((tokens, n)) if out_dtype is None or out_dtype is x.dtype else x.new_empty((tokens, n), dtype=out_dtype)
         ldy = n
     else:
@@ -524,6 +532,8 @@ def mx_matvec(fmt: Format, w: QTensor, x: torch.Tensor, bias=None, y=None, out_d
     q = _PACK_QTENSOR(codes.data_ptr(), scales.data_ptr(), offsets or 0, macro or 0, ts or 0, 0, n, k)
     _check(lib().mx_matvec(f, q, _code(x.dtype), x.data_ptr(), tokens, ldx, bp, y.data_ptr(), ldy, _code(y.dtype),
                            _stream_ptr(dev, "mx_matvec")), "mx_matvec")
+    if given:
+        _changed(y)
     return y
 
 
@@ -573,7 +583,7 @@ def mx_qk_rope(q, k, cos, sin, positions, q_weight=None, k_weight=None, eps=1e-6
         return _on(stream, mx_qk_rope, q, k, cos, sin, positions, q_weight, k_weight, eps, interleaved, q_out, k_out)
     if q.dim() != 3:
         raise ValueError("mx_qk_rope: q must be tokens x heads x dim")
-    dev, dim = q.get_device(), q.size(2)
+    dev, dim, given = q.get_device(), q.size(2), (q_out, k_out)
     r = _rope_args(q, k, cos, sin, positions, q_weight, k_weight, eps, interleaved, "mx_qk_rope")
     hq = _heads(q, dim, dev, "mx_qk_rope: q")
     q_out, oq = _out_heads(q_out, q, dim, dev, "mx_qk_rope: q_out")
@@ -582,6 +592,8 @@ def mx_qk_rope(q, k, cos, sin, positions, q_weight=None, k_weight=None, eps=1e-6
         hk = _heads(k, dim, dev, "mx_qk_rope: k")
         k_out, ok = _out_heads(k_out, k, dim, dev, "mx_qk_rope: k_out")
     _check(lib().mx_qk_rope(r, hq, hk, oq, ok, _stream_ptr(dev, "mx_qk_rope")), "mx_qk_rope")
+    if given[0] is not None or given[1] is not None:
+        _changed(*given)
     return q_out, k_out
 
 
@@ -602,7 +614,7 @@ def mx_qk_rope_backward(dy_q, dy_k, q, k, cos, sin, positions, q_weight=None, k_
                    workspace)
     if q.dim() != 3 or (k is None) != (dy_k is None):
         raise ValueError("mx_qk_rope_backward: q must be tokens x heads x dim, and dy_k and k go together")
-    dev, dim = q.get_device(), q.size(2)
+    dev, dim, given = q.get_device(), q.size(2), (dq, dk)
     r = _rope_args(q, k, cos, sin, positions, q_weight, k_weight, eps, interleaved, "mx_qk_rope_backward")
     if dy_q.shape != q.shape or (k is not None and dy_k.shape != k.shape):
         raise ValueError("mx_qk_rope_backward: gradients must have their heads' shape")
@@ -621,6 +633,8 @@ def mx_qk_rope_backward(dy_q, dy_k, q, k, cos, sin, positions, q_weight=None, k_
     _check(lib().mx_qk_rope_backward(r, gq, gk, xq, xk, oq, ok, _raw(dqw), _raw(dkw), _raw(workspace),
                                      0 if workspace is None else workspace.nbytes, _stream_ptr(dev, "mx_qk_rope_backward")),
            "mx_qk_rope_backward")
+    if given[0] is not None or given[1] is not None:
+        _changed(*given)
     return dq, dk, dqw, dkw
 
 
@@ -724,6 +738,7 @@ def mx_attend(q, cache: KVCache, page_table, lengths, scale=None, out=None, lse=
     if last != 1 and cols > 1 and batch:
         raise ValueError("mx_attend: the rows of page_table must be contiguous")
     n = _vector(lengths, batch, torch.int32, dev, "mx_attend", "lengths")
+    given = (out, None if lse is True else lse)
     out, ho = _out_heads(out, q, dim, dev, "mx_attend: out")
     if lse is True:
         lse = q.new_empty((batch, heads), dtype=torch.float32)
@@ -737,4 +752,6 @@ def mx_attend(q, cache: KVCache, page_table, lengths, scale=None, out=None, lse=
     _check(lib().mx_attend(cache._ref, hq, batch, page_table.data_ptr(), cols, cols if batch <= 1 else stride, n,
                            dim ** -0.5 if scale is None else scale, ho, _raw(lse), workspace.data_ptr(), workspace.nbytes,
                            _stream_ptr(dev, "mx_attend")), "mx_attend")
+    if given[0] is not None or given[1] is not None:
+        _changed(*given)
     return out if lse is None else (out, lse)
