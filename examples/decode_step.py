@@ -10,6 +10,7 @@ import os
 import sys
 
 import torch
+from torch.autograd.function import once_differentiable
 
 sys.path.insert(0, os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
 import microscaling_block_quantization_amd as mx  # noqa: E402
@@ -52,7 +53,7 @@ class AttentionLayer:
 
 
 class QKRope(torch.autograd.Function):
-    """mx_qk_rope and its gradient for training."""
+    """mx_qk_rope and its gradient for training; k and either weight may be None."""
 
     @staticmethod
     def forward(ctx, q, k, cos, sin, positions, q_weight, k_weight, eps):
@@ -61,10 +62,13 @@ class QKRope(torch.autograd.Function):
         return mx.mx_qk_rope(q, k, cos, sin, positions, q_weight, k_weight, eps)
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dy_q, dy_k):
         q, k, cos, sin, positions, qw, kw = ctx.saved_tensors
-        dq, dk, dqw, dkw = mx.mx_qk_rope_backward(dy_q.contiguous(), dy_k.contiguous(), q, k, cos, sin, positions, qw, kw, ctx.eps)
-        return dq, dk, None, None, None, dqw.to(qw.dtype), dkw.to(kw.dtype), None
+        dense = lambda t: None if t is None else t.contiguous()
+        dq, dk, dqw, dkw = mx.mx_qk_rope_backward(dense(dy_q), dense(dy_k), q, k, cos, sin, positions, qw, kw, ctx.eps)
+        like = lambda g, w: None if w is None else g.to(w.dtype)
+        return dq, dk, None, None, None, like(dqw, qw), like(dkw, kw), None
 
 
 def main():
