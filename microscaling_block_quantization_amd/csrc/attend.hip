@@ -337,7 +337,11 @@ __device__ __forceinline__ bool share_of(int64_t batch, uint32_t w, int workers,
 template <int D, int KIND, bool QF32, bool PAGE16, int AW>
 __global__ __launch_bounds__(64 * AW, D <= 128 ? 2 : 1) void k_attend(AttendParams p) {
     constexpr int QP = QF32 ? 3 : 1;              // bf16 parts of a query
-    constexpr int PP = QF32 ? 3 : 2;              // bf16 parts of a probability
+    // bf16 parts of a probability: three hold all its 24 bits.  A bf16 query's
+    // output has 8, and a probability's 16 move it by at most 2^-16 of sum p |v|
+    // (one in a few hundred outputs rounds to its other bf16 neighbour; the error
+    // against 64 bits is the same), for two products instead of three.
+    constexpr int PP = QF32 ? 3 : 2;
     constexpr int BITS = kind_bits(KIND), ROWB = D * BITS / 8, NB = D / 32;
     constexpr int KU = count_units(D, unit_max(KIND));     // units of the score product
     constexpr int VU = count_units(D, 128);                // runs of 16 lanes of the second product
@@ -840,7 +844,11 @@ constexpr int64_t FULL = 256;          // whole sequences that fill the chip, on
 // token's row is 256 bytes or more, so that four waves keep enough in flight,
 // three where it is less (us with 256 workgroups and with 768, 32 sequences up
 // to 8192 tokens of 128 values: bf16 106 and 120, MXFP8 84 and 68, MXFP4 71 and
-// 52; bf16 of 64 values, half the tokens: 44 and 37).
+// 52; bf16 of 64 values, half the tokens: 44 and 37).  Those are pages of a
+// multiple of 16 and bf16 queries, whose registers (up to 168) let a CU hold the
+// three.  Of the 44 variants below 256 bytes 29 hold one or two (other pages or
+// fp32 queries at 96 and 128 values, fp32 queries of other pages at 64, all at
+// 192 and 256) and run the 768 in rounds; their counts were not measured.
 AttendPlan attend_plan(const KvCache& c, int64_t batch, int q_heads, int64_t cols) {
     const int64_t planes = planes_of(c, q_heads), longest = cols * c.page;
     if (c.dim <= EIGHT_MAX && (longest <= 8 * TILE || (longest <= 8 * TILE * 4 && batch * planes >= FULL))) return AttendPlan{8, 0};

@@ -61,3 +61,30 @@ def test_whole_sequences_of_other_heads(dim, group):
     out, lse = mx.mx_attend(q, cache, table, n, lse=True, workspace=torch.empty(0, device="cuda", dtype=torch.uint8))
     some = [0, 1, 2, 63, 127, int(n.argmax()), int(n.argmin())]
     check_attend(cache, table[some], n[some], q[some], dim ** -0.5, out[some], lse[some], f"{dim} {group}")
+
+
+@pytest.mark.parametrize("dim", [128, 256])
+def test_wide_head_tiles_in_a_graph(dim):
+    """16 query heads of a key-value head take over 64 KiB of LDS, which a
+    launch asks for; captured, every replay (its query renewed) is the eager
+    call's, bit for bit."""
+    lengths = [200, 0, 77]
+    cache, table, n = build("bf16", lengths, 2, dim, 16)
+    g = torch.Generator(device="cuda").manual_seed(5)
+    q = torch.randn(3, 32, dim, device="cuda", generator=g).to(BF16)
+    ws = mx.alloc_attend_workspace(cache, 3, 32, table.shape[1])
+    held = q.clone()
+    mx.mx_attend(held, cache, table, n, workspace=ws)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out, lse = mx.mx_attend(held, cache, table, n, lse=True, workspace=ws)
+    for i in range(6):
+        held.copy_(torch.randn(3, 32, dim, device="cuda", generator=g))
+        ws.fill_(0xFF)
+        graph.replay()
+        want, wl = mx.mx_attend(held, cache, table, n, lse=True)
+        if i % 3 == 0:
+            torch.cuda.synchronize()
+        assert torch.equal(out, want) and torch.equal(lse, wl), f"replay {i}"
+    check_attend(cache, table, n, held, dim ** -0.5, out, lse, f"{dim}")
