@@ -427,7 +427,8 @@ int mx_cache_write(const mx_kv_cache *cache, const mx_heads *k, const mx_heads *
  *    at and past a length is not used, whatever it holds.  A page number
  *    outside the cache makes its sequence's outputs NaN.
  *  - Scores, softmax statistics and sums are fp32.  A bf16 q multiplies the
- *    cache's exact values; fp32 q enters as the exact sum of three bf16 parts.
+ *    cache's exact values; fp32 q enters as the exact sum of three bf16 parts
+ *    (multiples of 2^-133).
  *    Probabilities enter the second product as two bf16 parts (16 bits; three
  *    parts for fp32), their sum in fp32.
  *  - The length is split over workgroups, their parts joined in a fixed order;

@@ -108,3 +108,28 @@ def test_quantize_and_products():
         assert pool_of(a.data_ptr()) == side.cuda_stream, i
     err, db = mx.mx_qsnr(x, x.clone(), stream=side)
     assert err["n"] == x.numel()
+
+
+def test_inside_a_graph():
+    """A captured stream that forks into the given one and joins it again:
+    every replay is the eager result, with the main stream's allocations in
+    between."""
+    call, _ = attend()
+    back, _ = rope_backward()
+    want = [t.clone() for t in (*call(), *back())]
+    side = torch.cuda.Stream()
+    graph = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph):
+        main = torch.cuda.current_stream()
+        side.wait_stream(main)
+        got = (*call(stream=side), *back(stream=side))
+        main.wait_stream(side)
+    for i in range(5):
+        for t in got:
+            t.fill_(float("nan"))
+        torch.full((1 << 20,), float("nan"), device="cuda")
+        graph.replay()
+        if i % 2:
+            torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, want)), f"replay {i}"
