@@ -320,7 +320,8 @@ int mx_gemm(const mx_format *fa, const mx_qtensor *a, const mx_format *fb,
  *    2D blocks): MX_ERR_UNSUPPORTED.
  *  - W's values enter exactly (decoded to bf16, which holds every code times
  *    its scale as multiples of 2^-133; INT4 as multiples of 2^-129, which only
- *    macro scales can need more of), an fp32 x as the exact sum of three bf16
+ *    macro scales can need more of; an E2M1 value past fp32's range makes its
+ *    row's outputs non-finite), an fp32 x as the exact sum of three bf16
  *    parts (multiples of 2^-133); products are summed in fp32 in a fixed order.
  *    An offset or the INT4 bias enters as offset times the block's sum of x
  *    (multiples of 2^-129 beside INT4 offsets).  Symmetric INT4 is (u - 8) s
