@@ -444,6 +444,41 @@ int mx_attend(const mx_kv_cache *cache, const mx_heads *q, int64_t batch, const 
               int64_t table_cols, int64_t table_stride, const int32_t *lengths, float scale,
               const mx_heads *out, float *lse, void *workspace, size_t ws_bytes, void *stream);
 
+/* Reads cached keys and values back: token i's, which lie where mx_cache_write
+ * puts slot slots[i], as cache->heads heads of cache->dim values in k and v
+ * (one dtype; no two places the same).  A code counts its value times its
+ * block's scale (NaN under scale code 255), rounded to nearest even for bf16
+ * outputs; a bf16 cache's values as they are.  A slot outside the cache reads
+ * as zeros.  One slot may come up any number of times.  Limits as
+ * mx_cache_write's.                                                          */
+int mx_cache_read(const mx_kv_cache *cache, const int64_t *slots, int64_t tokens, const mx_heads *k,
+                  const mx_heads *v, void *stream);
+
+/* ---- many requests on one base model ----------------------------------------
+ * A batch whose requests share the quantized model and a prompt.             */
+
+/* mx_attend for sequences that share their first tokens: sequence b and query
+ * head h attend over the prefix's tokens, t < *prefix_length at
+ * prefix_table[t / page_size], and then over the sequence's own, t <
+ * lengths[b] by page_table and lengths as in mx_attend.  The result is
+ * mx_attend's for the prefix's and the own tokens as one sequence; the prefix
+ * is read once for all sequences (for up to 128 pairs of a sequence and a query
+ * head of one key-value head, and once more for each further 128).
+ *  - prefix_table, prefix_length (one number): int32 on the device.
+ *    *prefix_length <= 0 is no prefix, one past the table counts as the table.
+ *    lengths[b] <= 0: the prefix alone.  Neither: out 0, lse -inf.  A page
+ *    outside the cache among the prefix's makes every sequence's outputs NaN.
+ *  - Everything else, rounding and order included, as mx_attend; the two agree
+ *    up to the order of sums in fp32.  workspace: at least
+ *    mx_attend_shared_workspace_size bytes for this batch and these columns,
+ *    which serves every smaller call over a cache of the same form.          */
+size_t mx_attend_shared_workspace_size(const mx_kv_cache *cache, int64_t batch, int32_t q_heads,
+                                       int64_t prefix_cols, int64_t table_cols);
+int mx_attend_shared(const mx_kv_cache *cache, const mx_heads *q, int64_t batch, const int32_t *prefix_table,
+                     int64_t prefix_cols, const int32_t *prefix_length, const int32_t *page_table,
+                     int64_t table_cols, int64_t table_stride, const int32_t *lengths, float scale,
+                     const mx_heads *out, float *lse, void *workspace, size_t ws_bytes, void *stream);
+
 /* Text for a status code (static storage). */
 const char *mx_status_string(int status);
 

@@ -37,7 +37,7 @@ DTYPE_F32, DTYPE_BF16 = range(2)
 EXPORTS = ["mx_query_sizes", "mx_quantize", "mx_quantize_noalloc", "mx_quantize_many", "mx_dequantize",
            "mx_qsnr_workspace_size", "mx_qsnr", "mx_gemm", "mx_matvec", "mx_qk_rope",
            "mx_qk_rope_workspace_size", "mx_qk_rope_backward", "mx_cache_write", "mx_attend_workspace_size",
-           "mx_attend", "mx_status_string"]
+           "mx_attend", "mx_cache_read", "mx_attend_shared_workspace_size", "mx_attend_shared", "mx_status_string"]
 
 
 class MxFormat(ctypes.Structure):
@@ -134,11 +134,15 @@ def lib():
         L.mx_attend_workspace_size.argtypes = [vp, i64, ctypes.c_int32, i64]
         L.mx_attend_workspace_size.restype = sz
         L.mx_attend.argtypes = [vp, vp, i64, vp, i64, i64, vp, ctypes.c_float, vp, vp, vp, sz, vp]
+        L.mx_cache_read.argtypes = [vp, vp, i64, vp, vp, vp]
+        L.mx_attend_shared_workspace_size.argtypes = [vp, i64, ctypes.c_int32, i64, i64]
+        L.mx_attend_shared_workspace_size.restype = sz
+        L.mx_attend_shared.argtypes = [vp, vp, i64, vp, i64, vp, vp, i64, i64, vp, ctypes.c_float, vp, vp, vp, sz, vp]
         L.mx_status_string.argtypes = [i32]
         L.mx_status_string.restype = ctypes.c_char_p
         for name in ("mx_query_sizes", "mx_quantize", "mx_quantize_noalloc", "mx_quantize_many",
                      "mx_dequantize", "mx_qsnr", "mx_gemm", "mx_matvec", "mx_qk_rope", "mx_qk_rope_backward",
-                     "mx_cache_write", "mx_attend"):
+                     "mx_cache_write", "mx_attend", "mx_cache_read", "mx_attend_shared"):
             getattr(L, name).restype = ctypes.c_int
         _lib = L
     return _lib
@@ -707,6 +711,30 @@ def mx_cache_write(cache: KVCache, k, v, slots, stream=None):
     return cache
 
 
+def mx_cache_read(cache: KVCache, slots, k=None, v=None, out_dtype=torch.bfloat16, stream=None):
+    """The keys and values that lie at `slots` (int64 per token, as
+    mx_cache_write takes them), dequantized: tokens x heads x dim each.  A slot
+    outside the cache reads as zeros.  k, v: tensors of one dtype to write into
+    (any token and head strides), else new ones of out_dtype (bf16 or fp32).
+    Returns (k, v)."""
+    if stream is not None:
+        return _on(stream, mx_cache_read, cache, slots, k, v, out_dtype)
+    dev, tokens, given = cache.k.get_device(), slots.numel(), (k, v)
+    at = _vector(slots, tokens, torch.int64, dev, "mx_cache_read", "slots")
+    shape = (tokens, cache.heads, cache.dim)
+    if k is None:
+        k = cache.k.new_empty(shape, dtype=out_dtype if v is None else v.dtype)
+    if v is None:
+        v = cache.k.new_empty(shape, dtype=k.dtype)
+    if k.shape != shape or v.shape != shape:
+        raise ValueError(f"mx_cache_read: k and v must be {shape}")
+    hk, hv = _heads(k, cache.dim, dev, "mx_cache_read: k"), _heads(v, cache.dim, dev, "mx_cache_read: v")
+    _check(lib().mx_cache_read(cache._ref, at, tokens, hk, hv, _stream_ptr(dev, "mx_cache_read")), "mx_cache_read")
+    if given[0] is not None or given[1] is not None:
+        _changed(*given)
+    return k, v
+
+
 def mx_attend_workspace_size(cache: KVCache, batch, q_heads, table_cols):
     """Workspace bytes of mx_attend for at most `batch` sequences of at most
     `table_cols` pages."""
@@ -752,6 +780,61 @@ def mx_attend(q, cache: KVCache, page_table, lengths, scale=None, out=None, lse=
     _check(lib().mx_attend(cache._ref, hq, batch, page_table.data_ptr(), cols, cols if batch <= 1 else stride, n,
                            dim ** -0.5 if scale is None else scale, ho, _raw(lse), workspace.data_ptr(), workspace.nbytes,
                            _stream_ptr(dev, "mx_attend")), "mx_attend")
+    if given[0] is not None or given[1] is not None:
+        _changed(*given)
+    return out if lse is None else (out, lse)
+
+
+# ---- many requests on one base model -----------------------------------------
+def mx_attend_shared_workspace_size(cache: KVCache, batch, q_heads, prefix_cols, table_cols):
+    """Workspace bytes of mx_attend_shared for at most `batch` sequences of at
+    most `table_cols` pages of their own behind at most `prefix_cols` shared ones."""
+    return int(lib().mx_attend_shared_workspace_size(cache._ref, batch, q_heads, prefix_cols, table_cols))
+
+
+def alloc_attend_shared_workspace(cache: KVCache, batch, q_heads, prefix_cols, table_cols):
+    """A workspace for calls of at most these sizes."""
+    return _empty(mx_attend_shared_workspace_size(cache, batch, q_heads, prefix_cols, table_cols), cache.k.device)
+
+
+def mx_attend_shared(q, cache: KVCache, prefix, prefix_length, page_table, lengths, scale=None, out=None, lse=None, workspace=None,
+                     stream=None):
+    """mx_attend for sequences that share their first tokens: one new token per
+    sequence over the shared prefix, read once for all, and the sequence's own
+    tokens after it.  prefix: int32 page numbers of the prefix; prefix_length:
+    one int32 on the device, its tokens.  page_table and lengths: each
+    sequence's own tokens alone, as in mx_attend (0 allowed; with an empty
+    prefix: out 0, lse -inf).  The other arguments and the result are
+    mx_attend's; workspace: as alloc_attend_shared_workspace gives."""
+    if stream is not None:
+        return _on(stream, mx_attend_shared, q, cache, prefix, prefix_length, page_table, lengths, scale, out, lse, workspace)
+    dev, dim = cache.k.get_device(), cache.dim
+    hq = _heads(q, dim, dev, "mx_attend_shared: q")
+    batch, heads = q.size(0), q.size(1)
+    if page_table.dim() != 2 or page_table.dtype != torch.int32 or page_table.size(0) != batch or page_table.get_device() != dev:
+        raise ValueError(f"mx_attend_shared: page_table must be {batch} rows of int32 on the cache's device")
+    cols = page_table.size(1)
+    stride, last = page_table.stride()
+    if last != 1 and cols > 1 and batch:
+        raise ValueError("mx_attend_shared: the rows of page_table must be contiguous")
+    n = _vector(lengths, batch, torch.int32, dev, "mx_attend_shared", "lengths")
+    ahead = prefix.numel()
+    pages = _vector(prefix, ahead, torch.int32, dev, "mx_attend_shared", "prefix")
+    pn = _vector(prefix_length, 1, torch.int32, dev, "mx_attend_shared", "prefix_length")
+    given = (out, None if lse is True else lse)
+    out, ho = _out_heads(out, q, dim, dev, "mx_attend_shared: out")
+    if lse is True:
+        lse = q.new_empty((batch, heads), dtype=torch.float32)
+    elif lse is not None and (lse.shape != (batch, heads) or lse.dtype != torch.float32 or not lse.is_contiguous() or
+                              lse.get_device() != dev):
+        raise ValueError(f"mx_attend_shared: lse must be a contiguous fp32 {batch} x {heads}")
+    if workspace is None:
+        workspace = cache.k.new_empty((lib().mx_attend_shared_workspace_size(cache._ref, batch, heads, ahead, cols),), dtype=torch.uint8)
+    elif workspace.get_device() != dev or not workspace.is_contiguous():
+        _buffer(workspace, 0, dev, "mx_attend_shared", "workspace")
+    _check(lib().mx_attend_shared(cache._ref, hq, batch, pages, ahead, pn, page_table.data_ptr(), cols,
+                                  cols if batch <= 1 else stride, n, dim ** -0.5 if scale is None else scale, ho, _raw(lse),
+                                  workspace.data_ptr(), workspace.nbytes, _stream_ptr(dev, "mx_attend_shared")), "mx_attend_shared")
     if given[0] is not None or given[1] is not None:
         _changed(*given)
     return out if lse is None else (out, lse)

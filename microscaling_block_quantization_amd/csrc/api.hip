@@ -347,6 +347,15 @@ size_t attend_bytes(const mx_kv_cache* c, int32_t q_heads, int64_t slots) {
     return round_up((size_t)q_heads * slots * (c->dim + 2) * sizeof(float));
 }
 
+// the workspace of an attention behind a shared prefix: the sequences' own parts
+// (of whole sequences too), then the prefix's
+size_t shared_bytes(const mx_kv_cache* c, int64_t batch, int32_t q_heads, int64_t prefix_cols, int64_t cols) {
+    const mxk::KvCache k = cache_params(c);
+    const int64_t slots = mxk::attend_slots(k, batch, q_heads, cols);
+    return attend_bytes(c, q_heads, slots > batch ? slots : batch) +
+           round_up((size_t)mxk::shared_rows(k, batch, q_heads, prefix_cols) * (c->dim + 2) * sizeof(float));
+}
+
 }  // namespace
 
 extern "C" {
@@ -804,6 +813,99 @@ int mx_attend(const mx_kv_cache* cache, const mx_heads* q, int64_t batch, const 
     p.waves = a.waves;
     p.workers = a.workers;
     return launch_status(mxk::launch_attend(p, q->dtype == MX_DTYPE_BF16, static_cast<hipStream_t>(stream)));
+}
+
+int mx_cache_read(const mx_kv_cache* cache, const int64_t* slots, int64_t tokens, const mx_heads* k, const mx_heads* v,
+                  void* stream) {
+    if (tokens < 0) return MX_ERR_ARG;
+    int rc = check_cache(cache, tokens > 0);
+    if (rc) return rc;
+    if (tokens == 0) return MX_OK;
+    for (const mx_heads* h : {k, v}) {
+        rc = check_heads(h, tokens);
+        if (rc) return rc;
+        if (h->heads != cache->heads || h->dtype != k->dtype) return MX_ERR_ARG;
+    }
+    if (!slots || tokens >= ((int64_t)1 << 30) / cache->heads) return MX_ERR_ARG;
+    if (!aligned_to(slots, 8)) return MX_ERR_ALIGN;
+    mxk::CacheRead p;
+    memset(&p, 0, sizeof(p));
+    p.c = cache_params(cache);
+    p.k = k->x;
+    p.v = v->x;
+    p.k_ts = k->token_stride;
+    p.k_hs = k->head_stride;
+    p.v_ts = v->token_stride;
+    p.v_hs = v->head_stride;
+    p.slots = slots;
+    p.tokens = tokens;
+    return launch_status(mxk::launch_cache_read(p, k->dtype == MX_DTYPE_BF16, static_cast<hipStream_t>(stream)));
+}
+
+size_t mx_attend_shared_workspace_size(const mx_kv_cache* cache, int64_t batch, int32_t q_heads, int64_t prefix_cols,
+                                       int64_t table_cols) {
+    if (check_cache(cache, false) || check_attend(cache, batch, q_heads, table_cols) ||
+        check_attend(cache, batch, q_heads, prefix_cols))
+        return 0;
+    return shared_bytes(cache, batch, q_heads, prefix_cols, table_cols);
+}
+
+int mx_attend_shared(const mx_kv_cache* cache, const mx_heads* q, int64_t batch, const int32_t* prefix_table,
+                     int64_t prefix_cols, const int32_t* prefix_length, const int32_t* page_table, int64_t table_cols,
+                     int64_t table_stride, const int32_t* lengths, float scale, const mx_heads* out, float* lse,
+                     void* workspace, size_t ws_bytes, void* stream) {
+    if (batch < 0 || table_cols < 0 || prefix_cols < 0) return MX_ERR_ARG;
+    int rc = check_cache(cache, batch > 0 && (table_cols > 0 || prefix_cols > 0));
+    if (rc) return rc;
+    if (batch == 0) return MX_OK;
+    for (const mx_heads* h : {q, out}) {
+        rc = check_heads(h, batch);
+        if (rc) return rc;
+    }
+    if (!same_heads(q, out)) return MX_ERR_ARG;
+    for (int64_t cols : {table_cols, prefix_cols}) {
+        rc = check_attend(cache, batch, q->heads, cols);
+        if (rc) return rc;
+    }
+    if (!lengths || !prefix_length || (table_cols && !page_table) || (prefix_cols && !prefix_table) ||
+        (batch > 1 && table_stride < table_cols))
+        return MX_ERR_ARG;
+    if (!aligned_to(lse, 4) || !aligned_to(lengths, 4) || !aligned_to(page_table, 4) || !aligned_to(prefix_table, 4) ||
+        !aligned_to(prefix_length, 4))
+        return MX_ERR_ALIGN;
+    const mxk::KvCache c = cache_params(cache);
+    const bool bf = q->dtype == MX_DTYPE_BF16;
+    const mxk::AttendPlan a = mxk::attend_plan(c, batch, q->heads, table_cols);
+    const mxk::SharedPlan b = mxk::shared_plan(c, batch, q->heads, prefix_cols, bf);
+    if (!workspace || ws_bytes < shared_bytes(cache, batch, q->heads, prefix_cols, table_cols)) return MX_ERR_WORKSPACE;
+    if (!aligned16(workspace)) return MX_ERR_ALIGN;
+    mxk::SharedParams p;
+    memset(&p, 0, sizeof(p));
+    p.own.c = c;
+    p.own.q = q->x;
+    p.own.q_ts = q->token_stride;
+    p.own.q_hs = q->head_stride;
+    p.own.o = out->x;
+    p.own.o_ts = out->token_stride;
+    p.own.o_hs = out->head_stride;
+    p.own.batch = batch;
+    p.own.q_heads = q->heads;
+    p.own.table = page_table;
+    p.own.cols = table_cols;
+    p.own.table_stride = table_stride;
+    p.own.lengths = lengths;
+    p.own.scale = scale;
+    p.own.lse = lse;
+    p.own.parts = static_cast<float*>(workspace);
+    p.own.waves = a.waves;
+    p.own.workers = a.workers;
+    p.prefix = prefix_table;
+    p.prefix_cols = prefix_cols;
+    p.prefix_length = prefix_length;
+    p.parts = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + attend_bytes(cache, q->heads, a.workers + batch));
+    p.row_waves = b.row_waves;
+    p.splits = b.splits;
+    return launch_status(mxk::launch_attend_shared(p, bf, static_cast<hipStream_t>(stream)));
 }
 
 }  // extern "C"

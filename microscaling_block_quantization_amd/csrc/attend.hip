@@ -29,34 +29,12 @@
 // tokens, bf16, 106 us, 5.3 TB/s of cache (a large copy reaches 5.1); one of
 // 131072, bf16 100 us (5.4), MXFP8 64 us (4.3), MXFP4 47 us (3.0), where the
 // conversions, the softmax and the waits between them no longer hide.
-#include "decode_kernels.hpp"
+#include "attend_device.hpp"
 
 namespace mxk {
 using namespace mxd;
 
 namespace {
-
-typedef __bf16 bf8v __attribute__((ext_vector_type(8)));
-typedef __bf16 bf2v __attribute__((ext_vector_type(2)));
-typedef float f2v __attribute__((ext_vector_type(2)));
-typedef float f4v __attribute__((ext_vector_type(4)));
-typedef short s2v __attribute__((ext_vector_type(2)));
-typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
-
-__device__ __forceinline__ float e8m0(uint32_t c) {
-    return c == 255u ? bitsf(0x7fc00000u) : bitsf(c ? c << 23 : 0x00400000u);
-}
-__device__ __forceinline__ uint32_t bits_of(bf2v v) {
-    uint32_t u;
-    __builtin_memcpy(&u, &v, 4);
-    return u;
-}
-__device__ __forceinline__ bf8v frag(uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
-    const uint32_t u[4] = {a, b, c, d};
-    bf8v v;
-    __builtin_memcpy(&v, u, 16);
-    return v;
-}
 
 // ---------------------------------------------------------------------------
 // Write: eight values a lane, four lanes a block.  The scale rule and the
@@ -65,17 +43,6 @@ __device__ __forceinline__ bf8v frag(uint32_t a, uint32_t b, uint32_t c, uint32_
 // ones it writes.
 // ---------------------------------------------------------------------------
 constexpr int CT = 256;
-
-// t / d for t < 2^31 by a multiply: mul = ceil(2^shift / d), 2^shift >= 2^31 d
-__device__ __forceinline__ uint32_t over(uint32_t t, Div d) { return (uint32_t)(((uint64_t)t * d.mul) >> d.shift); }
-Div div_by(int d) {
-    int lg = 0;
-    while ((1 << lg) < d) lg++;
-    Div o;
-    o.shift = 31 + lg;
-    o.mul = (uint32_t)((((uint64_t)1 << o.shift) + d - 1) / d);
-    return o;
-}
 
 // D: the head dimension, known here because a division by a number that is not
 // costs more than everything else a lane does.  A lane takes the key and the
@@ -152,6 +119,63 @@ __global__ __launch_bounds__(CT) void k_cache_write(CacheWrite p) {
 }
 
 // ---------------------------------------------------------------------------
+// Read: the write's lanes the other way round.  A code's value times its block's
+// power of two is exact in fp32, so the one rounding is a bf16 output's.
+// ---------------------------------------------------------------------------
+template <int D, int KIND, bool BF>
+__global__ __launch_bounds__(CT) void k_cache_read(CacheRead p) {
+    constexpr uint32_t UNITS = D / 8, PER = CT / UNITS;           // lanes of a vector, vectors of a workgroup
+    constexpr int BITS = kind_bits(KIND);
+    const uint32_t n = threadIdx.x / UNITS, u = threadIdx.x - n * UNITS;
+    const uint32_t item = blockIdx.x * PER + n;                   // (token, head)
+    const uint32_t token = over(item, p.per_token), head = item - token * p.c.heads;
+    if (n >= PER || (int64_t)token >= p.tokens) return;
+    const int64_t slot = p.slots[token];
+    const bool in = slot >= 0 && slot < p.c.pages * p.c.page;     // outside: zeros
+    const int64_t at = in ? slot : 0;
+    const int64_t page = p.page_shift >= 0 ? at >> p.page_shift : at < (1ll << 31) ? over((uint32_t)at, p.page_div) : at / p.c.page;
+    const int64_t row = (page * p.c.heads + head) * p.c.page + (at - page * p.c.page);
+    uint32_t raw[2][4], sc[2];
+#pragma unroll
+    for (int v = 0; v < 2; v++) {
+        load_bytes<BITS>(raw[v], (v ? p.c.v : p.c.k) + (row * D + 8 * u) * BITS / 8);
+        if constexpr (KIND != KV_BF16) sc[v] = (v ? p.c.vs : p.c.ks)[row * (D / 32) + u / 4];
+    }
+#pragma unroll
+    for (int v = 0; v < 2; v++) {
+        float x[8];
+        if constexpr (KIND == KV_BF16) {
+#pragma unroll
+            for (int e = 0; e < 8; e++) x[e] = (e & 1) ? bf16hi(raw[v][e / 2]) : bf16lo(raw[v][e / 2]);
+        } else {
+            const float s = e8m0(sc[v]);
+            each<4>([&](auto ic) {
+                constexpr int I = ic.value;
+                f2v w;
+                if constexpr (KIND == KV_FP8) w = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8((int)raw[v][I / 2], 1.0f, (I & 1) != 0);
+                else w = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(raw[v][0], 1.0f, I);
+                x[2 * I] = w[0] * s;
+                x[2 * I + 1] = w[1] * s;
+            });
+        }
+        const int64_t dst = (int64_t)token * (v ? p.v_ts : p.k_ts) + (int64_t)head * (v ? p.v_hs : p.k_hs) + 8 * u;
+        if constexpr (BF) {
+            u32x4 o;
+#pragma unroll
+            for (int e = 0; e < 4; e++) {
+                const f2v xy = {x[2 * e], x[2 * e + 1]};
+                o[e] = !in ? 0u : KIND == KV_BF16 ? raw[v][e] : bits_of(__builtin_convertvector(xy, bf2v));
+            }
+            *reinterpret_cast<u32x4*>(static_cast<uint16_t*>(v ? p.v : p.k) + dst) = o;
+        } else {
+            f4v* o = reinterpret_cast<f4v*>(static_cast<float*>(v ? p.v : p.k) + dst);
+            o[0] = in ? f4v{x[0], x[1], x[2], x[3]} : f4v{0.f, 0.f, 0.f, 0.f};
+            o[1] = in ? f4v{x[4], x[5], x[6], x[7]} : f4v{0.f, 0.f, 0.f, 0.f};
+        }
+    }
+}
+
+// ---------------------------------------------------------------------------
 // Attention
 // ---------------------------------------------------------------------------
 constexpr int TILE = 32;               // tokens a wave takes at a time
@@ -160,7 +184,6 @@ constexpr int EIGHT_MAX = 128;         // largest head dimension whose registers
 
 // Bits of one value, and the widest run of the head dimension (a "unit") that
 // 4 lanes of a token cover with one load of at most 16 bytes each.
-constexpr int kind_bits(int kind) { return kind == KV_BF16 ? 16 : kind == KV_FP8 ? 8 : 4; }
 constexpr int unit_max(int kind) { return 4 * 128 / kind_bits(kind); }
 // the unit at `base`: the widest power of two that fits, at least 32
 constexpr int unit_at(int D, int base, int most) {
@@ -179,58 +202,6 @@ constexpr int unit_base(int D, int most, int i) {
     return b;
 }
 
-// `bytes` (4, 8 or 16; 1 or 2 for small V runs) from p into dwords of o
-template <int BYTES>
-__device__ __forceinline__ void load_bytes(uint32_t* o, const uint8_t* p) {
-    if constexpr (BYTES == 16) {
-        const u32x4 v = *reinterpret_cast<const u32x4*>(p);
-        o[0] = v[0]; o[1] = v[1]; o[2] = v[2]; o[3] = v[3];
-    } else if constexpr (BYTES == 8) {
-        const u32x2 v = *reinterpret_cast<const u32x2*>(p);
-        o[0] = v[0]; o[1] = v[1];
-    } else if constexpr (BYTES == 4) {
-        o[0] = *reinterpret_cast<const uint32_t*>(p);
-    } else if constexpr (BYTES == 2) {
-        o[0] = *reinterpret_cast<const uint16_t*>(p);
-    } else {
-        o[0] = *p;
-    }
-}
-
-// values 2 i, 2 i + 1 of the run in w as a bf16 pair times 2^e
-template <int KIND, int I>
-__device__ __forceinline__ uint32_t pair_of(const uint32_t* w, float s) {
-    if constexpr (KIND == KV_BF16) return w[I];
-    else if constexpr (KIND == KV_FP8) return bits_of(__builtin_amdgcn_cvt_scalef32_pk_bf16_fp8((int)w[I / 2], s, (I & 1) != 0));
-    else return bits_of(__builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w[I / 4], s, I & 3));
-}
-
-template <int... I>
-struct seq {};
-template <int N, int... I>
-struct make_seq : make_seq<N - 1, N - 1, I...> {};
-template <int... I>
-struct make_seq<0, I...> { typedef seq<I...> type; };
-// f(integral_constant 0), ... f(integral_constant N - 1)
-template <int V>
-struct ic { static constexpr int value = V; };
-template <typename F, int... I>
-__device__ __forceinline__ void each_(F&& f, seq<I...>) { (f(ic<I>{}), ...); }
-template <int N, typename F>
-__device__ __forceinline__ void each(F&& f) { each_(f, typename make_seq<N>::type{}); }
-
-// a query value as its exact bf16 parts (bits in the upper halves)
-struct Parts {
-    uint32_t h, m, l;
-};
-__device__ __forceinline__ Parts parts_of(float x) {
-    const uint32_t u = fbits(x);
-    if ((u & 0x7f800000u) == 0x7f800000u) return Parts{(uint32_t)bf16_rne(x) << 16, 0u, 0u};
-    const float r = x - bitsf(u & 0xffff0000u);
-    return Parts{u & 0xffff0000u, fbits(r) & 0xffff0000u, fbits(r - bitsf(fbits(r) & 0xffff0000u)) & 0xffff0000u};
-}
-__device__ __forceinline__ uint32_t pack_hi(uint32_t a, uint32_t b) { return __builtin_amdgcn_perm(b, a, 0x07060302u); }
-
 // Left to itself the scheduler moves loads behind the wait for older ones.
 #define ISSUED __builtin_amdgcn_sched_barrier(0)
 
@@ -242,24 +213,6 @@ __device__ __forceinline__ uint32_t pack_hi(uint32_t a, uint32_t b) { return __b
 // sequence and the beginning of the next; a sequence within one range is
 // finished there, the others' parts go to slot w + b of their heads (in order, a
 // range's step moves w on and a sequence's step b, so no two share one).
-constexpr int UNIT = 128;
-__device__ __forceinline__ int64_t units_of(int len) { return (len + UNIT - 1) / UNIT; }
-
-__device__ __forceinline__ int workers_used(int64_t units, int workers) { return (int)(units < workers ? units : workers); }
-
-// sum over the workgroup of T threads, in every thread
-template <int T>
-__device__ __forceinline__ int64_t block_total(int64_t v, int64_t* sh) {
-#pragma unroll
-    for (int o = 1; o < 64; o <<= 1) v += __shfl_xor(v, o, 64);
-    if ((threadIdx.x & 63) == 0) sh[threadIdx.x >> 6] = v;
-    __syncthreads();
-    int64_t t = 0;
-#pragma unroll
-    for (int i = 0; i < T / 64; i++) t += sh[i];
-    __syncthreads();
-    return t;
-}
 // Worker w's range, the sequence its first unit lies in and the units before
 // that sequence; false for an empty range.
 template <int T, typename F>
@@ -652,14 +605,15 @@ __global__ __launch_bounds__(64 * AW, D <= 128 ? 2 : 1) void k_attend(AttendPara
             o += f * sums[(w * nh + h) * LD + d];
         }
         const int64_t bh = b * p.q_heads + h0 + h;
-        if (t0 == 0 && tend == len) {                      // the whole sequence
+        if (!p.all_parts && t0 == 0 && tend == len) {      // the whole sequence
             const float v = L == 0.f ? 0.f : o / L;
             const int64_t at = b * p.o_ts + (int64_t)(h0 + h) * p.o_hs + d;
             if (QF32) static_cast<float*>(p.o)[at] = v;
             else static_cast<uint16_t*>(p.o)[at] = bf16_rne(v);
             if (p.lse && d == 0) p.lse[bh] = L == 0.f ? -INFINITY : (Ms + log2f(L)) * 0.69314718055994530942f;
         } else {
-            const int64_t slots = p.workers + p.batch, at = (h0 + h) * slots + (int64_t)(blockIdx.x - plane * (uint32_t)p.workers) + b;
+            const int64_t w = p.workers ? blockIdx.x - plane * (uint32_t)p.workers : 0;
+            const int64_t slots = p.workers + p.batch, at = (h0 + h) * slots + w + b;
             p.parts[at * D + d] = o;
             if (d == 0) {
                 float* x = p.parts + (int64_t)p.q_heads * slots * D + at * 2;
@@ -772,7 +726,7 @@ template <int D, int KIND, bool QF32, bool PAGE16, int AW>
 hipError_t go(const AttendParams& p, hipStream_t s) {
     const int group = p.q_heads / p.c.heads, tiles = (group + QH - 1) / QH, rows = group < QH ? group : QH;
     const int64_t n = p.c.heads * tiles * (p.workers ? p.workers : p.batch);
-    const int64_t joins = p.workers ? p.batch * p.q_heads : 0;
+    const int64_t joins = p.workers && !p.all_parts ? p.batch * p.q_heads : 0;
     if (!grid_ok(n, 64 * AW) || !grid_ok(joins, 256)) return TOO_LARGE;
     const int lds = AW * rows * (D + 3) * (int)sizeof(float);
     if (lds > 64 * 1024) {
@@ -815,7 +769,37 @@ hipError_t write_dim(const CacheWrite& p, bool bf, hipStream_t s) {
     return p.c.kind == KV_FP8 ? write_as<D, KV_FP8>(p, bf, s) : write_as<D, KV_FP4>(p, bf, s);
 }
 
+template <int D, int KIND>
+hipError_t read_as(const CacheRead& p, bool bf, hipStream_t s) {
+    constexpr int PER = CT / (D / 8);
+    const int64_t n = p.tokens * p.c.heads;
+    if (!grid_ok((n + PER - 1) / PER, CT)) return TOO_LARGE;
+    const unsigned grid = (unsigned)((n + PER - 1) / PER);
+    if (bf) k_cache_read<D, KIND, true><<<grid, CT, 0, s>>>(p);
+    else k_cache_read<D, KIND, false><<<grid, CT, 0, s>>>(p);
+    return hipGetLastError();
+}
+template <int D>
+hipError_t read_dim(const CacheRead& p, bool bf, hipStream_t s) {
+    if (p.c.kind == KV_BF16) return read_as<D, KV_BF16>(p, bf, s);
+    return p.c.kind == KV_FP8 ? read_as<D, KV_FP8>(p, bf, s) : read_as<D, KV_FP4>(p, bf, s);
+}
+
 }  // namespace
+
+hipError_t launch_cache_read(CacheRead p, bool bf, hipStream_t s) {
+    p.per_token = div_by(p.c.heads);
+    p.page_div = div_by(p.c.page);
+    p.page_shift = -1;
+    if ((p.c.page & (p.c.page - 1)) == 0) p.page_shift = __builtin_ctz((unsigned)p.c.page);
+    switch (p.c.dim) {
+    case 64: return read_dim<64>(p, bf, s);
+    case 96: return read_dim<96>(p, bf, s);
+    case 128: return read_dim<128>(p, bf, s);
+    case 192: return read_dim<192>(p, bf, s);
+    default: return read_dim<256>(p, bf, s);
+    }
+}
 
 hipError_t launch_cache_write(CacheWrite p, bool bf, hipStream_t s) {
     p.per_token = div_by(p.c.heads);

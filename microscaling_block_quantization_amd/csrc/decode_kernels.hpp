@@ -93,6 +93,7 @@ struct AttendParams {
     float* lse;                    // nullable
     float* parts;                  // with workers: [q head][worker + sequence][dim] sums, then [..][2] max and sum
     int waves, workers;            // of the plan
+    int all_parts;                 // whole sequences go to `parts` too, and nothing is joined
     Div page_div;                  // set by the launcher
 };
 // How a call is split: waves per workgroup; 0, or the workgroups that share the
@@ -106,5 +107,37 @@ AttendPlan attend_plan(const KvCache& c, int64_t batch, int q_heads, int64_t col
 int64_t attend_slots(const KvCache& c, int64_t batch, int q_heads, int64_t cols);
 bool attend_dim_ok(int dim);
 hipError_t launch_attend(AttendParams p, bool q_bf16, hipStream_t s);
+
+// Attention of sequences behind one shared prefix.  `own`: the sequences' own
+// tokens (all_parts set, parts as without it; slots there are workers + batch).
+struct SharedParams {
+    AttendParams own;
+    const int32_t* prefix;         // its pages
+    int64_t prefix_cols;
+    const int32_t* prefix_length;  // one number
+    float* parts;                  // of the prefix: [plane][split][row][dim] sums, then [..][2] max and sum
+    int row_waves, splits;         // of the plan
+};
+// How the prefix is split: rows (a sequence's query heads of one key-value head)
+// in tiles of 32 row_waves, its tokens in `splits` ranges for each tile
+struct SharedPlan {
+    int row_waves, splits;
+    int64_t planes;                // tiles of rows of all key-value heads
+};
+SharedPlan shared_plan(const KvCache& c, int64_t batch, int q_heads, int64_t prefix_cols, bool q_bf16);
+// Rows of prefix parts, at most, of any call of at most this batch and these columns
+int64_t shared_rows(const KvCache& c, int64_t batch, int q_heads, int64_t prefix_cols);
+hipError_t launch_attend_shared(SharedParams p, bool q_bf16, hipStream_t s);
+
+struct CacheRead {
+    KvCache c;
+    void *k, *v;
+    int64_t k_ts, k_hs, v_ts, v_hs;
+    const int64_t* slots;
+    int64_t tokens;
+    Div per_token, page_div;       // set by the launcher
+    int page_shift;
+};
+hipError_t launch_cache_read(CacheRead p, bool out_bf16, hipStream_t s);
 
 }  // namespace mxk
