@@ -479,6 +479,39 @@ int mx_attend_shared(const mx_kv_cache *cache, const mx_heads *q, int64_t batch,
                      int64_t table_cols, int64_t table_stride, const int32_t *lengths, float scale,
                      const mx_heads *out, float *lse, void *workspace, size_t ws_bytes, void *stream);
 
+/* Low-rank adapters of one projection (n outputs, k inputs; the struct is host
+ * memory).  a: count x rank x k and b: count x n x rank, dense, of `dtype`
+ * (fp32 or bf16); scales (nullable: all 1): count fp32.  rank: a multiple of 8
+ * up to 256 (pad with zeros); k: a multiple of 8 (MX_ERR_UNSUPPORTED
+ * otherwise), below 2^24; n < 2^31.                                          */
+typedef struct mx_adapters {
+    const void *a, *b;
+    const float *scales;
+    int64_t k, n;
+    int32_t count, rank, dtype;
+} mx_adapters;
+
+/* y[t] = base[t] + scales[i] b_i (a_i x[t]) with i = ids[t]: what each token's
+ * request adds to a shared projection, such as mx_matvec's or mx_gemm's.  x:
+ * tokens x k of the adapters' dtype (row stride ldx, a multiple of 16 bytes);
+ * ids: int32 on the device; base (nullable: zero): tokens x n of base_dtype,
+ * row stride ld_base; y: tokens x n of y_dtype, row stride ldy, rounded once,
+ * to nearest even.  y may be base itself (same dtype and stride), else must
+ * not overlap an input.
+ *  - An id outside 0 .. count - 1 names no adapter: y[t] = base[t].  Tokens
+ *    may come in any order; the adapters are read once for each 16 tokens in
+ *    a row that name them, so tokens of one adapter are best side by side.
+ *  - Products and sums are fp32 (a x too: bf16 operands enter exactly, and the
+ *    rank values enter the second product as exact sums of three bf16 parts,
+ *    multiples of 2^-133).  A NaN or Inf in a token's x reaches its y alone.
+ *  - workspace: at least mx_lora_workspace_size(a, tokens) bytes, which serves
+ *    fewer tokens and smaller ranks too; no initial contents needed; calls that
+ *    share one must not overlap.  tokens <= 2^24.                             */
+size_t mx_lora_workspace_size(const mx_adapters *a, int64_t tokens);
+int mx_lora(const mx_adapters *a, const void *x, int64_t tokens, int64_t ldx, const int32_t *ids, int base_dtype,
+            const void *base, int64_t ld_base, int y_dtype, void *y, int64_t ldy, void *workspace, size_t ws_bytes,
+            void *stream);
+
 /* Text for a status code (static storage). */
 const char *mx_status_string(int status);
 

@@ -37,7 +37,8 @@ DTYPE_F32, DTYPE_BF16 = range(2)
 EXPORTS = ["mx_query_sizes", "mx_quantize", "mx_quantize_noalloc", "mx_quantize_many", "mx_dequantize",
            "mx_qsnr_workspace_size", "mx_qsnr", "mx_gemm", "mx_matvec", "mx_qk_rope",
            "mx_qk_rope_workspace_size", "mx_qk_rope_backward", "mx_cache_write", "mx_attend_workspace_size",
-           "mx_attend", "mx_cache_read", "mx_attend_shared_workspace_size", "mx_attend_shared", "mx_status_string"]
+           "mx_attend", "mx_cache_read", "mx_attend_shared_workspace_size", "mx_attend_shared",
+           "mx_lora_workspace_size", "mx_lora", "mx_status_string"]
 
 
 class MxFormat(ctypes.Structure):
@@ -93,6 +94,11 @@ class MxKVCache(ctypes.Structure):
                 ("page_size", ctypes.c_int32), ("heads", ctypes.c_int32), ("dim", ctypes.c_int32)]
 
 
+class MxAdapters(ctypes.Structure):
+    _fields_ = [("a", ctypes.c_void_p), ("b", ctypes.c_void_p), ("scales", ctypes.c_void_p), ("k", ctypes.c_int64),
+                ("n", ctypes.c_int64), ("count", ctypes.c_int32), ("rank", ctypes.c_int32), ("dtype", ctypes.c_int32)]
+
+
 class MxError(RuntimeError):
     def __init__(self, status, where):
         self.status = status
@@ -138,11 +144,14 @@ def lib():
         L.mx_attend_shared_workspace_size.argtypes = [vp, i64, ctypes.c_int32, i64, i64]
         L.mx_attend_shared_workspace_size.restype = sz
         L.mx_attend_shared.argtypes = [vp, vp, i64, vp, i64, vp, vp, i64, i64, vp, ctypes.c_float, vp, vp, vp, sz, vp]
+        L.mx_lora_workspace_size.argtypes = [vp, i64]
+        L.mx_lora_workspace_size.restype = sz
+        L.mx_lora.argtypes = [vp, vp, i64, i64, vp, i32, vp, i64, i32, vp, i64, vp, sz, vp]
         L.mx_status_string.argtypes = [i32]
         L.mx_status_string.restype = ctypes.c_char_p
         for name in ("mx_query_sizes", "mx_quantize", "mx_quantize_noalloc", "mx_quantize_many",
                      "mx_dequantize", "mx_qsnr", "mx_gemm", "mx_matvec", "mx_qk_rope", "mx_qk_rope_backward",
-                     "mx_cache_write", "mx_attend", "mx_cache_read", "mx_attend_shared"):
+                     "mx_cache_write", "mx_attend", "mx_cache_read", "mx_attend_shared", "mx_lora"):
             getattr(L, name).restype = ctypes.c_int
         _lib = L
     return _lib
@@ -838,3 +847,79 @@ def mx_attend_shared(q, cache: KVCache, prefix, prefix_length, page_table, lengt
     if given[0] is not None or given[1] is not None:
         _changed(*given)
     return out if lse is None else (out, lse)
+
+
+@dataclass(frozen=True, eq=False)
+class Adapters:
+    """Low-rank adapters of one projection: a (count x rank x K) and b (count x
+    N x rank), both bf16 or both fp32; scales: None or fp32 per adapter.  rank
+    and K are multiples of 8.  Fixed once made: its C struct is packed here."""
+    a: torch.Tensor
+    b: torch.Tensor
+    scales: torch.Tensor = None
+
+    def __post_init__(self):
+        a, b, s = self.a, self.b, self.scales
+        if a.dim() != 3 or b.dim() != 3 or a.size(0) != b.size(0) or a.size(1) != b.size(2):
+            raise ValueError("Adapters: a must be count x rank x K and b count x N x rank")
+        if a.dtype != b.dtype or a.get_device() != b.get_device() or not a.is_contiguous() or not b.is_contiguous():
+            raise ValueError("Adapters: a and b must be contiguous, of one dtype, on one device")
+        if s is not None and (s.shape != (a.size(0),) or s.dtype != torch.float32 or not s.is_contiguous() or
+                              s.get_device() != a.get_device()):
+            raise ValueError(f"Adapters: scales must be {a.size(0)} contiguous fp32 values on the adapters' device")
+        c = MxAdapters(a.data_ptr(), b.data_ptr(), _raw(s), a.size(2), b.size(1), a.size(0), a.size(1), _code(a.dtype))
+        object.__setattr__(self, "_c", c)
+        object.__setattr__(self, "_ref", ctypes.byref(c))
+
+
+def mx_lora_workspace_size(adapters: Adapters, tokens):
+    """Workspace bytes of mx_lora for at most `tokens` tokens."""
+    return int(lib().mx_lora_workspace_size(adapters._ref, tokens))
+
+
+def alloc_lora_workspace(adapters: Adapters, tokens):
+    """A workspace for calls of at most `tokens` tokens."""
+    return _empty(mx_lora_workspace_size(adapters, tokens), adapters.a.device)
+
+
+def mx_lora(x, adapters: Adapters, ids, base=None, y=None, out_dtype=None, workspace=None, stream=None):
+    """y[t] = base[t] + scales[i] b_i (a_i x[t]), i = ids[t]: the adapters of
+    many requests beside a shared projection (base: mx_matvec's or mx_gemm's
+    output, bf16 or fp32, any row stride; None: zero).  x: tokens x K of the
+    adapters' dtype; ids: int32 per token, one outside 0 .. count - 1 (-1, say)
+    names none.  y: a tokens x N view to write into (base itself included),
+    else a new tensor of out_dtype (default: base's, without one x's)."""
+    if stream is not None:
+        return _on(stream, mx_lora, x, adapters, ids, base, y, out_dtype, workspace)
+    a = adapters.a
+    dev, k, n, shape = a.get_device(), a.size(2), adapters.b.size(1), x.shape
+    if len(shape) != 2 or shape[1] != k or x.get_device() != dev or x.dtype != a.dtype:
+        raise ValueError(f"mx_lora: x must be tokens x {k} of the adapters' dtype on their device")
+    tokens = shape[0]
+    ldx, last = x.stride()
+    if last != 1 and k > 1 and tokens:
+        raise ValueError("mx_lora: the rows of x must be contiguous")
+    at = _vector(ids, tokens, torch.int32, dev, "mx_lora", "ids")
+    ldb, bd = n, DTYPE_F32
+    if base is not None:
+        if base.shape != (tokens, n) or (base.stride(1) != 1 and n > 1 and tokens) or base.get_device() != dev:
+            raise ValueError(f"mx_lora: base must be {tokens} x {n} with contiguous rows")
+        ldb, bd = base.stride(0), _code(base.dtype)
+    given, ldy = y is not None, n
+    if not given:
+        y = x.new_empty((tokens, n), dtype=out_dtype or (x if base is None else base).dtype)
+    else:
+        if y.shape != (tokens, n) or (y.stride(1) != 1 and n > 1 and tokens) or y.get_device() != dev:
+            raise ValueError(f"mx_lora: y must be {tokens} x {n} with contiguous rows")
+        ldy = y.stride(0)
+    if tokens <= 1:
+        ldx, ldb, ldy = k, n, n
+    if workspace is None:
+        workspace = x.new_empty((lib().mx_lora_workspace_size(adapters._ref, tokens),), dtype=torch.uint8)
+    elif workspace.get_device() != dev or not workspace.is_contiguous():
+        _buffer(workspace, 0, dev, "mx_lora", "workspace")
+    _check(lib().mx_lora(adapters._ref, x.data_ptr(), tokens, ldx, at, bd, _raw(base), ldb, _code(y.dtype), y.data_ptr(), ldy,
+                         workspace.data_ptr(), workspace.nbytes, _stream_ptr(dev, "mx_lora")), "mx_lora")
+    if given:
+        _changed(y)
+    return y

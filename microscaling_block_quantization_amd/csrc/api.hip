@@ -356,6 +356,15 @@ size_t shared_bytes(const mx_kv_cache* c, int64_t batch, int32_t q_heads, int64_
            round_up((size_t)mxk::shared_rows(k, batch, q_heads, prefix_cols) * (c->dim + 2) * sizeof(float));
 }
 
+// The adapters of a call.
+constexpr int64_t MAX_LORA_TOKENS = 1 << 24;
+int check_adapters(const mx_adapters* a) {
+    if (!a || !dtype_ok(a->dtype) || a->count < 0 || a->k < 0 || a->n < 0) return MX_ERR_ARG;
+    if (a->rank < 8 || a->rank > 256 || a->rank % 8 || a->k % 8 || a->k == 0) return MX_ERR_UNSUPPORTED;
+    if (a->k >= (int64_t)1 << 24 || a->n >= (int64_t)1 << 31) return MX_ERR_ARG;
+    return MX_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -906,6 +915,52 @@ int mx_attend_shared(const mx_kv_cache* cache, const mx_heads* q, int64_t batch,
     p.row_waves = b.row_waves;
     p.splits = b.splits;
     return launch_status(mxk::launch_attend_shared(p, bf, static_cast<hipStream_t>(stream)));
+}
+
+size_t mx_lora_workspace_size(const mx_adapters* a, int64_t tokens) {
+    if (check_adapters(a) || tokens <= 0 || tokens > MAX_LORA_TOKENS) return 0;
+    return round_up((size_t)mxk::lora_rows(tokens) * a->rank * sizeof(float));
+}
+
+int mx_lora(const mx_adapters* a, const void* x, int64_t tokens, int64_t ldx, const int32_t* ids, int base_dtype,
+            const void* base, int64_t ld_base, int y_dtype, void* y, int64_t ldy, void* workspace, size_t ws_bytes,
+            void* stream) {
+    int rc = check_adapters(a);
+    if (rc) return rc;
+    if (!dtype_ok(y_dtype) || (base && !dtype_ok(base_dtype)) || tokens < 0 || tokens > MAX_LORA_TOKENS) return MX_ERR_ARG;
+    if (ldx < a->k || ldy < a->n || (base && ld_base < a->n)) return MX_ERR_ARG;
+    if (tokens == 0 || a->n == 0) return MX_OK;
+    if (!x || !y || !ids || (a->count && (!a->a || !a->b))) return MX_ERR_ARG;
+    if (base == y && base && (ld_base != ldy || base_dtype != y_dtype)) return MX_ERR_ARG;
+    if (!aligned16(x) || !aligned16(base) || !aligned16(y) || !aligned16(a->a) || !aligned16(a->b) || !aligned_to(a->scales, 4) ||
+        !aligned_to(ids, 4) || (tokens > 1 && ((ldx * elem_size(a->dtype)) & 15)))
+        return MX_ERR_ALIGN;
+    if (!workspace || ws_bytes < mx_lora_workspace_size(a, tokens)) return MX_ERR_WORKSPACE;
+    if (!aligned16(workspace)) return MX_ERR_ALIGN;
+    mxk::LoraParams p;
+    memset(&p, 0, sizeof(p));
+    p.a = a->a;
+    p.b = a->b;
+    p.scales = a->scales;
+    p.count = a->count;
+    p.rank = a->rank;
+    p.bf16 = a->dtype == MX_DTYPE_BF16;
+    p.k = a->k;
+    p.n = a->n;
+    p.x = x;
+    p.tokens = tokens;
+    p.ldx = ldx;
+    p.ids = ids;
+    p.base = base;
+    p.ld_base = ld_base;
+    p.y = y;
+    p.ldy = ldy;
+    p.base_bf16 = base_dtype == MX_DTYPE_BF16;
+    p.y_bf16 = y_dtype == MX_DTYPE_BF16;
+    p.vec_base = tokens <= 1 || ((ld_base * elem_size(base_dtype)) & 15) == 0;
+    p.vec_y = tokens <= 1 || ((ldy * elem_size(y_dtype)) & 15) == 0;
+    p.h = static_cast<float*>(workspace);
+    return launch_status(mxk::launch_lora(p, static_cast<hipStream_t>(stream)));
 }
 
 }  // extern "C"

@@ -140,4 +140,24 @@ struct CacheRead {
 };
 hipError_t launch_cache_read(CacheRead p, bool out_bf16, hipStream_t s);
 
+struct LoraParams {
+    const void *a, *b;             // count x rank x k, count x n x rank
+    const float* scales;           // nullable: count
+    int count, rank, bf16;         // bf16: type of x, a and b
+    int64_t k, n;
+    const void* x;                 // tokens x k, row stride ldx
+    int64_t tokens, ldx;
+    const int32_t* ids;
+    const void* base;              // nullable: tokens x n
+    int64_t ld_base;
+    void* y;
+    int64_t ldy;
+    int base_bf16, y_bf16, vec_base, vec_y;      // vec: rows start at multiples of 16 bytes
+    float* h;                      // [split][token][rank]
+    int splits, spread, rank_groups, run;        // set by the launcher
+};
+// Rows of h, at most, of any call of at most this many tokens
+int64_t lora_rows(int64_t tokens);
+hipError_t launch_lora(LoraParams p, hipStream_t s);
+
 }  // namespace mxk
