@@ -512,6 +512,37 @@ int mx_lora(const mx_adapters *a, const void *x, int64_t tokens, int64_t ldx, co
             const void *base, int64_t ld_base, int y_dtype, void *y, int64_t ldy, void *workspace, size_t ws_bytes,
             void *stream);
 
+/* What a step's logits say of given tokens: for each row z of logits (tokens x
+ * vocab, row stride ld >= vocab, any; fp32 or bf16)
+ *   lse = log sum_j exp(z_j),  logprob = z[target] - lse,
+ *   entropy = -sum_j p_j log p_j  with p_j = exp(z_j - lse),
+ * and, where top > 0, the `top` (at most 64 and vocab) likeliest: top_ids and
+ * top_logprobs (tokens x top, dense), likeliest first, equal logits by the lower
+ * id.  targets: int64; one outside 0 .. vocab - 1 has logprob 0 (padding).
+ *  - Logits of -Inf (masked tokens) have probability 0 and count nothing.  A row
+ *    of them alone: lse, logprob and top_logprobs -Inf, entropy 0.  A row with
+ *    a NaN or +Inf: everything NaN (a padding target's logprob stays 0), the
+ *    top_ids some ids of the vocabulary.
+ *  - fp32 throughout, sums in an order fixed by the sizes and by where rows
+ *    start against 16 bytes.  workspace: at least mx_logprobs_workspace_size
+ *    bytes, which serves every smaller call; may be NULL where the row count
+ *    alone fills the chip (1024 tokens or more).                             */
+size_t mx_logprobs_workspace_size(int64_t tokens, int64_t vocab, int32_t top);
+int mx_logprobs(int dtype, const void *logits, int64_t tokens, int64_t vocab, int64_t ld, const int64_t *targets,
+                float *logprob, float *lse, float *entropy, int32_t top, float *top_logprobs, int64_t *top_ids,
+                void *workspace, size_t ws_bytes, void *stream);
+
+/* The gradient of logprob and entropy: with g = d_logprob[t] and e =
+ * d_entropy[t] (either NULL: zero),
+ *   d_logits[j] = g (1[j = target] - p_j) - e p_j (log p_j + entropy)
+ * of the logits' dtype, row stride ld_d, rounded once; d_logits may be the
+ * logits themselves (same stride).  lse and entropy: as mx_logprobs gave them
+ * (entropy only where d_entropy is set).  A target outside the vocabulary has
+ * no gradient of its logprob; a row without a possible token, none at all.    */
+int mx_logprobs_backward(int dtype, const float *d_logprob, const float *d_entropy, const void *logits,
+                         int64_t tokens, int64_t vocab, int64_t ld, const int64_t *targets, const float *lse,
+                         const float *entropy, void *d_logits, int64_t ld_d, void *stream);
+
 /* Text for a status code (static storage). */
 const char *mx_status_string(int status);
 

@@ -38,7 +38,8 @@ EXPORTS = ["mx_query_sizes", "mx_quantize", "mx_quantize_noalloc", "mx_quantize_
            "mx_qsnr_workspace_size", "mx_qsnr", "mx_gemm", "mx_matvec", "mx_qk_rope",
            "mx_qk_rope_workspace_size", "mx_qk_rope_backward", "mx_cache_write", "mx_attend_workspace_size",
            "mx_attend", "mx_cache_read", "mx_attend_shared_workspace_size", "mx_attend_shared",
-           "mx_lora_workspace_size", "mx_lora", "mx_status_string"]
+           "mx_lora_workspace_size", "mx_lora", "mx_logprobs_workspace_size", "mx_logprobs", "mx_logprobs_backward",
+           "mx_status_string"]
 
 
 class MxFormat(ctypes.Structure):
@@ -147,11 +148,16 @@ def lib():
         L.mx_lora_workspace_size.argtypes = [vp, i64]
         L.mx_lora_workspace_size.restype = sz
         L.mx_lora.argtypes = [vp, vp, i64, i64, vp, i32, vp, i64, i32, vp, i64, vp, sz, vp]
+        L.mx_logprobs_workspace_size.argtypes = [i64, i64, ctypes.c_int32]
+        L.mx_logprobs_workspace_size.restype = sz
+        L.mx_logprobs.argtypes = [i32, vp, i64, i64, i64, vp, vp, vp, vp, ctypes.c_int32, vp, vp, vp, sz, vp]
+        L.mx_logprobs_backward.argtypes = [i32, vp, vp, vp, i64, i64, i64, vp, vp, vp, vp, i64, vp]
         L.mx_status_string.argtypes = [i32]
         L.mx_status_string.restype = ctypes.c_char_p
         for name in ("mx_query_sizes", "mx_quantize", "mx_quantize_noalloc", "mx_quantize_many",
                      "mx_dequantize", "mx_qsnr", "mx_gemm", "mx_matvec", "mx_qk_rope", "mx_qk_rope_backward",
-                     "mx_cache_write", "mx_attend", "mx_cache_read", "mx_attend_shared", "mx_lora"):
+                     "mx_cache_write", "mx_attend", "mx_cache_read", "mx_attend_shared", "mx_lora",
+                     "mx_logprobs", "mx_logprobs_backward"):
             getattr(L, name).restype = ctypes.c_int
         _lib = L
     return _lib
@@ -923,3 +929,82 @@ def mx_lora(x, adapters: Adapters, ids, base=None, y=None, out_dtype=None, works
     if given:
         _changed(y)
     return y
+
+
+def mx_logprobs_workspace_size(tokens, vocab, top=0):
+    """Workspace bytes of mx_logprobs for at most these sizes."""
+    return int(lib().mx_logprobs_workspace_size(tokens, vocab, top))
+
+
+def alloc_logprobs_workspace(tokens, vocab, top=0, device="cuda"):
+    """A workspace for calls of at most these sizes."""
+    return _empty(mx_logprobs_workspace_size(tokens, vocab, top), device)
+
+
+def _logits(z, targets, where):
+    """tokens, vocab, row stride and the targets' address of a matrix of logits."""
+    if z.dim() != 2 or z.size(1) < 1:
+        raise ValueError(f"{where}: logits must be tokens x vocabulary")
+    tokens, vocab = z.shape
+    ld, last = z.stride()
+    if last != 1 and vocab > 1 and tokens:
+        raise ValueError(f"{where}: the rows of the logits must be contiguous")
+    return tokens, vocab, vocab if tokens <= 1 else ld, _vector(targets, tokens, torch.int64, z.get_device(), where, "targets")
+
+
+def mx_logprobs(logits, targets, top=0, workspace=None, stream=None):
+    """Log probability of each row's target, with lse and entropy, and the `top`
+    (0 .. 64) likeliest alternatives.  logits: tokens x vocabulary, bf16 or fp32,
+    any row stride; -Inf masks a token.  targets: int64 per token, one outside
+    the vocabulary (padding) has log probability 0.  workspace: as
+    alloc_logprobs_workspace gives (allocated when None).  Returns (logprob, lse,
+    entropy), fp32 per token, and with top also (top_logprobs, top_ids), tokens x
+    top in falling order, equal logits by the lower id."""
+    if stream is not None:
+        return _on(stream, mx_logprobs, logits, targets, top, workspace)
+    dev = logits.get_device()
+    tokens, vocab, ld, at = _logits(logits, targets, "mx_logprobs")
+    if not 0 <= top <= min(64, vocab):
+        raise ValueError(f"mx_logprobs: top must be 0 .. {min(64, vocab)}")
+    made = logits.new_empty((3 + top, tokens), dtype=torch.float32)
+    logprob, lse, entropy = made[:3]
+    tops = ids = None
+    if top:
+        tops, ids = made[3:].view(tokens, top), logits.new_empty((tokens, top), dtype=torch.int64)
+    if workspace is None:
+        workspace = logits.new_empty((lib().mx_logprobs_workspace_size(tokens, vocab, top),), dtype=torch.uint8)
+    elif workspace.get_device() != dev or not workspace.is_contiguous():
+        _buffer(workspace, 0, dev, "mx_logprobs", "workspace")
+    p = made.data_ptr()
+    _check(lib().mx_logprobs(_code(logits.dtype), logits.data_ptr(), tokens, vocab, ld, at, p, p + 4 * tokens, p + 8 * tokens, top,
+                             p + 12 * tokens if top else 0, _raw(ids), workspace.data_ptr(), workspace.nbytes,
+                             _stream_ptr(dev, "mx_logprobs")), "mx_logprobs")
+    return (logprob, lse, entropy, tops, ids) if top else (logprob, lse, entropy)
+
+
+def mx_logprobs_backward(d_logprob, d_entropy, logits, targets, lse, entropy=None, d_logits=None, stream=None):
+    """Gradient of mx_logprobs' logprob and entropy by the logits: d_logprob and
+    d_entropy are theirs, fp32 per token (either may be None), lse and entropy
+    its results.  d_logits: a tensor of the logits' shape and dtype to write into
+    (the logits themselves included), else a new one.  Returns d_logits."""
+    if stream is not None:
+        return _on(stream, mx_logprobs_backward, d_logprob, d_entropy, logits, targets, lse, entropy, d_logits)
+    dev = logits.get_device()
+    tokens, vocab, ld, at = _logits(logits, targets, "mx_logprobs_backward")
+    if d_entropy is not None and entropy is None:
+        raise ValueError("mx_logprobs_backward: d_entropy needs entropy")
+    need = lambda t, name: 0 if t is None else _vector(t, tokens, torch.float32, dev, "mx_logprobs_backward", name)
+    gl, gh, pl, ph = need(d_logprob, "d_logprob"), need(d_entropy, "d_entropy"), need(lse, "lse"), need(entropy, "entropy")
+    given, ldd = d_logits is not None, vocab
+    if not given:
+        d_logits = logits.new_empty((tokens, vocab))
+    else:
+        if (d_logits.shape != logits.shape or d_logits.dtype != logits.dtype or d_logits.get_device() != dev or
+                (d_logits.stride(1) != 1 and vocab > 1 and tokens)):
+            raise ValueError(f"mx_logprobs_backward: d_logits must be {tokens} x {vocab} of the logits' dtype with contiguous rows")
+        ldd = vocab if tokens <= 1 else d_logits.stride(0)
+    _check(lib().mx_logprobs_backward(_code(logits.dtype), gl, gh, logits.data_ptr(), tokens, vocab, ld, at, pl, ph,
+                                      d_logits.data_ptr(), ldd, _stream_ptr(dev, "mx_logprobs_backward")), "mx_logprobs_backward")
+    if given:
+        _changed(d_logits)
+    return d_logits

@@ -21,7 +21,7 @@ CEIL_SOURCES = ["ceilings.hip"]
 BUILD = os.path.join(HERE, "_build")
 SOURCES = ["api.hip", "quant_rows.hip", "quant_tiles.hip", "misc.hip", "gemm_mxfp4.hip", "gemm_lds.hip", "gemm_upcvt.hip",
            "matvec.hip", "qk_rope.hip", "attend.hip", "attend_shared.hip",
-           "lora.hip"]
+           "lora.hip", "logprobs.hip"]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 FLAGS = ["--offload-arch=gfx950", "-O3", "-std=c++17", "-fPIC",

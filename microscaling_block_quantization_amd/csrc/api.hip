@@ -365,6 +365,14 @@ int check_adapters(const mx_adapters* a) {
     return MX_OK;
 }
 
+// A matrix of logits.
+int check_logits(int64_t tokens, int64_t vocab, int64_t ld, int dtype) {
+    if (!dtype_ok(dtype) || tokens < 0 || tokens >= (int64_t)1 << 31 || vocab < 1 || vocab >= (int64_t)1 << 31 || ld < vocab)
+        return MX_ERR_ARG;
+    if ((double)tokens * ld >= 9.0e17) return MX_ERR_ARG;
+    return MX_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -961,6 +969,76 @@ int mx_lora(const mx_adapters* a, const void* x, int64_t tokens, int64_t ldx, co
     p.vec_y = tokens <= 1 || ((ldy * elem_size(y_dtype)) & 15) == 0;
     p.h = static_cast<float*>(workspace);
     return launch_status(mxk::launch_lora(p, static_cast<hipStream_t>(stream)));
+}
+
+size_t mx_logprobs_workspace_size(int64_t tokens, int64_t vocab, int32_t top) {
+    if (check_logits(tokens, vocab, vocab, MX_DTYPE_F32) || top < 0 || top > mxk::MOST_TOP || top > vocab) return 0;
+    return round_up((size_t)mxk::logprob_bytes(tokens, vocab, top));
+}
+
+int mx_logprobs(int dtype, const void* logits, int64_t tokens, int64_t vocab, int64_t ld, const int64_t* targets,
+                float* logprob, float* lse, float* entropy, int32_t top, float* top_logprobs, int64_t* top_ids,
+                void* workspace, size_t ws_bytes, void* stream) {
+    int rc = check_logits(tokens, vocab, ld, dtype);
+    if (rc) return rc;
+    if (top < 0 || top > vocab) return MX_ERR_ARG;
+    if (top > mxk::MOST_TOP) return MX_ERR_UNSUPPORTED;
+    if (tokens == 0) return MX_OK;
+    if (!logits || !targets || !logprob || !lse || !entropy || (top && (!top_logprobs || !top_ids))) return MX_ERR_ARG;
+    if (!aligned16(logits) || !aligned_to(targets, 8) || !aligned_to(logprob, 4) || !aligned_to(lse, 4) ||
+        !aligned_to(entropy, 4) || !aligned_to(top_logprobs, 4) || !aligned_to(top_ids, 8))
+        return MX_ERR_ALIGN;
+    const bool bf = dtype == MX_DTYPE_BF16;
+    const mxk::LogprobPlan a = mxk::logprob_plan(tokens, vocab, top, bf);
+    if (a.splits > 1) {
+        if (!workspace || ws_bytes < mx_logprobs_workspace_size(tokens, vocab, top)) return MX_ERR_WORKSPACE;
+        if (!aligned16(workspace)) return MX_ERR_ALIGN;
+    }
+    mxk::LogprobParams p;
+    memset(&p, 0, sizeof(p));
+    p.z = logits;
+    p.tokens = tokens;
+    p.vocab = vocab;
+    p.ld = ld;
+    p.targets = targets;
+    p.logprob = logprob;
+    p.lse = lse;
+    p.entropy = entropy;
+    p.top = top;
+    p.top_logprobs = top_logprobs;
+    p.top_ids = top_ids;
+    p.parts = workspace;
+    p.keys = reinterpret_cast<uint64_t*>(static_cast<uint8_t*>(workspace) + round_up((size_t)tokens * a.splits * 3 * sizeof(float)));
+    p.splits = a.splits;
+    p.segments = a.segments;
+    return launch_status(mxk::launch_logprobs(p, bf, static_cast<hipStream_t>(stream)));
+}
+
+int mx_logprobs_backward(int dtype, const float* d_logprob, const float* d_entropy, const void* logits, int64_t tokens,
+                         int64_t vocab, int64_t ld, const int64_t* targets, const float* lse, const float* entropy,
+                         void* d_logits, int64_t ld_d, void* stream) {
+    int rc = check_logits(tokens, vocab, ld, dtype);
+    if (rc) return rc;
+    if (ld_d < vocab) return MX_ERR_ARG;
+    if (tokens == 0) return MX_OK;
+    if (!logits || !targets || !lse || !d_logits || (d_entropy && !entropy) || (d_logits == logits && ld != ld_d)) return MX_ERR_ARG;
+    if (!aligned16(logits) || !aligned16(d_logits) || !aligned_to(targets, 8) || !aligned_to(lse, 4) ||
+        !aligned_to(entropy, 4) || !aligned_to(d_logprob, 4) || !aligned_to(d_entropy, 4))
+        return MX_ERR_ALIGN;
+    mxk::LogprobBackParams p;
+    memset(&p, 0, sizeof(p));
+    p.z = logits;
+    p.tokens = tokens;
+    p.vocab = vocab;
+    p.ld = ld;
+    p.targets = targets;
+    p.lse = lse;
+    p.entropy = d_entropy ? entropy : nullptr;
+    p.d_logprob = d_logprob;
+    p.d_entropy = d_entropy;
+    p.dz = d_logits;
+    p.ld_dz = ld_d;
+    return launch_status(mxk::launch_logprobs_back(p, dtype == MX_DTYPE_BF16, static_cast<hipStream_t>(stream)));
 }
 
 }  // extern "C"

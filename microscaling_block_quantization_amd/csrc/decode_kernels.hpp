@@ -160,4 +160,36 @@ struct LoraParams {
 int64_t lora_rows(int64_t tokens);
 hipError_t launch_lora(LoraParams p, hipStream_t s);
 
+constexpr int MOST_TOP = 64;       // alternatives of a row
+constexpr int MOST_KEYS = 1024;    // those of all its splits
+struct LogprobParams {
+    const void* z;                 // tokens x vocab, row stride ld
+    int64_t tokens, vocab, ld;
+    const int64_t* targets;
+    float *logprob, *lse, *entropy;
+    int top;
+    float* top_logprobs;           // tokens x top
+    int64_t* top_ids;
+    void* parts;                   // with several splits: [token][split] three numbers
+    uint64_t* keys;                // and [token][split][top]
+    int splits, segments;          // of the plan
+};
+struct LogprobPlan {
+    int splits, segments;
+};
+LogprobPlan logprob_plan(int64_t tokens, int64_t vocab, int top, bool bf16);
+int64_t logprob_bytes(int64_t tokens, int64_t vocab, int top);
+hipError_t launch_logprobs(const LogprobParams& p, bool bf16, hipStream_t s);
+
+struct LogprobBackParams {
+    const void* z;
+    int64_t tokens, vocab, ld;
+    const int64_t* targets;
+    const float *lse, *entropy, *d_logprob, *d_entropy;      // the last three nullable
+    void* dz;
+    int64_t ld_dz;
+    int splits;                    // set by the launcher
+};
+hipError_t launch_logprobs_back(LogprobBackParams p, bool bf16, hipStream_t s);
+
 }  // namespace mxk
