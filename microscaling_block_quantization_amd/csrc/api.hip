@@ -922,6 +922,7 @@ int mx_attend_shared(const mx_kv_cache* cache, const mx_heads* q, int64_t batch,
     p.parts = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + attend_bytes(cache, q->heads, a.workers + batch));
     p.row_waves = b.row_waves;
     p.splits = b.splits;
+    p.one = b.one;
     return launch_status(mxk::launch_attend_shared(p, bf, static_cast<hipStream_t>(stream)));
 }
 

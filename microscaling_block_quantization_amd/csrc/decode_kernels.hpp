@@ -117,12 +117,14 @@ struct SharedParams {
     const int32_t* prefix_length;  // one number
     float* parts;                  // of the prefix: [plane][split][row][dim] sums, then [..][2] max and sum
     int row_waves, splits;         // of the plan
+    bool one;
 };
 // How the prefix is split: rows (a sequence's query heads of one key-value head)
 // in tiles of 32 row_waves, its tokens in `splits` ranges for each tile
 struct SharedPlan {
     int row_waves, splits;
     int64_t planes;                // tiles of rows of all key-value heads
+    bool one;                      // few rows, and every range at most 64 tokens
 };
 SharedPlan shared_plan(const KvCache& c, int64_t batch, int q_heads, int64_t prefix_cols, bool q_bf16);
 // Rows of prefix parts, at most, of any call of at most this batch and these columns
