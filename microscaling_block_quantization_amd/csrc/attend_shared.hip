@@ -8,6 +8,17 @@
 // `batch x group` rows, each cached value read once for all.  The own tokens
 // are k_attend's, which leaves all its triples unjoined; k_shared_join adds
 // both kinds up.
+//
+// Bound and measured (32 query and 8 key-value heads of 128).  Few rows: memory;
+// 4 sequences behind 65536 bf16 tokens 61 us in all, 4.4 TB/s of cache.  Many:
+// issue slots, most of them the vector unit's (softmax, conversion of cached
+// values to bf16, two bf16 parts of every probability).  64 sequences behind 32768
+// MXFP8 tokens: 63 us for the prefix, 830 TFLOP/s of matrix instructions, of
+// which the second part of the probabilities takes 11 (one part: 52 us; it would
+// double the squared error against 64 bits, so it stays).  Tried there: 4 waves
+// to a workgroup, two of those on a CU, one copy of each tile and two barriers a
+// step 66 us; two groups of waves half a period apart 72 to 80; instruction order
+// by scheduling groups within 1 us of the compiler's.
 #include "attend_device.hpp"
 
 namespace mxk {
@@ -59,8 +70,7 @@ constexpr int lds_bytes(int D, int waves, int rw) {
 // that keeps the matrix and the vector unit busy at once.
 //
 // ONE: every range is one tile, so there is nothing to load ahead and four waves
-// do (one of 64 rows and tokens of a short prefix: 4 sequences on 777 tokens,
-// XXX us, with the other form 13).
+// do (4 sequences behind 777 bf16 tokens: 7.2 us, with the other form 13).
 template <int D, int KIND, bool QF32, int RW, bool ONE>
 __global__ __launch_bounds__(64 * waves_of(D, QF32, ONE), waves_of(D, QF32, ONE) / 4) void k_prefix(SharedParams p) {
     constexpr int W = waves_of(D, QF32, ONE), ST = 64 * W, TW = W / RW, TK = tile_tokens(W, RW), RT = 32 * RW;
@@ -543,8 +553,10 @@ template <int D, int KIND, bool QF32>
 hipError_t rows(const SharedParams& p, hipStream_t s) {
     if constexpr (waves_of(D, QF32) == 8)
         if (p.row_waves == 8) return go<D, KIND, QF32, 8, false>(p, s);
-    if (p.row_waves == 4) return go<D, KIND, QF32, 4, false>(p, s);
-    return p.one ? go<D, KIND, QF32, 2, true>(p, s) : go<D, KIND, QF32, 2, false>(p, s);
+    if (p.one) return go<D, KIND, QF32, 2, true>(p, s);
+    if constexpr (KIND != KV_BF16)
+        if (p.row_waves == 2) return go<D, KIND, QF32, 2, false>(p, s);
+    return go<D, KIND, QF32, 4, false>(p, s);
 }
 template <int D, bool QF32>
 hipError_t pick(const SharedParams& p, hipStream_t s) {
@@ -564,16 +576,18 @@ constexpr int FULL = 256;              // workgroups that fill the chip: one for
 
 // Tiles of 64, 128 or 256 rows (waves of rows that do not exist stand idle, which
 // few rows leave them time for), and as many ranges of tokens as fill the chip
-// once.
+// once.  64 rows stand with twice the tokens of 128 in a tile, for which a bf16
+// cache lacks registers: 4 sequences (16 rows) behind 65536 tokens take 53 us so
+// and 61 in tiles of 128 rows from MXFP8, 49 and 60 from MXFP4, but 63 and 61
+// from bf16.  A prefix that 64-token ranges cover takes those.
 SharedPlan shared_plan(const KvCache& c, int64_t batch, int q_heads, int64_t prefix_cols, bool q_bf16) {
-    const int64_t rows = batch * (q_heads / c.heads);
+    const int64_t rows = batch * (q_heads / c.heads), units = (prefix_cols * c.page + UT - 1) / UT;
     SharedPlan o;
-    o.row_waves = rows <= 64 ? 2 : rows <= 128 || waves_of(c.dim, !q_bf16) == 4 ? 4 : 8;
+    o.one = rows <= 64 && units <= FULL / c.heads;
+    o.row_waves = o.one || (rows <= 64 && c.kind != KV_BF16) ? 2 : rows <= 128 || waves_of(c.dim, !q_bf16) == 4 ? 4 : 8;
     o.planes = c.heads * ((rows + 32 * o.row_waves - 1) / (32 * o.row_waves));
-    const int64_t units = (prefix_cols * c.page + UT - 1) / UT;
     int64_t splits = o.planes ? FULL / o.planes : 1;
     if (splits < 1) splits = 1;
-    o.one = o.row_waves == 2 && units <= splits;
     o.splits = (int)(splits < units ? splits : units);
     return o;
 }
