@@ -990,7 +990,7 @@ int mx_logprobs(int dtype, const void* logits, int64_t tokens, int64_t vocab, in
         !aligned_to(entropy, 4) || !aligned_to(top_logprobs, 4) || !aligned_to(top_ids, 8))
         return MX_ERR_ALIGN;
     const bool bf = dtype == MX_DTYPE_BF16;
-    const mxk::LogprobPlan a = mxk::logprob_plan(tokens, vocab, top, bf);
+    const mxk::LogprobPlan a = mxk::logprob_plan(tokens, vocab, ld, top, bf);
     if (a.splits > 1) {
         if (!workspace || ws_bytes < mx_logprobs_workspace_size(tokens, vocab, top)) return MX_ERR_WORKSPACE;
         if (!aligned16(workspace)) return MX_ERR_ALIGN;

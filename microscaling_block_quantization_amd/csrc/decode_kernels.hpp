@@ -179,7 +179,7 @@ struct LogprobParams {
 struct LogprobPlan {
     int splits, segments;
 };
-LogprobPlan logprob_plan(int64_t tokens, int64_t vocab, int top, bool bf16);
+LogprobPlan logprob_plan(int64_t tokens, int64_t vocab, int64_t ld, int top, bool bf16);
 int64_t logprob_bytes(int64_t tokens, int64_t vocab, int top);
 hipError_t launch_logprobs(const LogprobParams& p, bool bf16, hipStream_t s);
 

@@ -7,7 +7,7 @@
 // (W + (m - m') S).  One pass over the logits, memory bound.  The gradient is
 //   dz_j = g (1[j = target] - p_j) - g_H p_j (ln p_j + H).
 //
-// Top alternatives.  A workgroup holds a segment of the row in registers, 32 KB.
+// Top alternatives.  A workgroup holds a segment of the row in registers, 16 KB.
 // The k-th largest of its 256 lanes' maxima bounds the k-th largest element from
 // below, and few elements besides the k largest reach it, so those are gathered
 // in LDS and ranked by counting.  The bound is found by bisection over the
@@ -22,7 +22,7 @@ namespace {
 typedef float f2v __attribute__((ext_vector_type(2)));
 typedef __bf16 bf2v __attribute__((ext_vector_type(2)));
 
-constexpr int LT = 256, NV = 8;                       // threads; 16-byte pieces of a lane in a segment
+constexpr int LT = 256, NV = 4;                       // threads; 16-byte pieces of a lane in a segment
 constexpr int EASY = 512;                             // candidates gathered without care for ties
 constexpr float FAR = -1e20f;                         // a distance whose exponential is 0 and whose products stay finite
 constexpr float LOG2E = 1.44269504088896340736f, LN2 = 0.69314718055994530942f;
@@ -80,6 +80,8 @@ __device__ __forceinline__ Triple wave_join(Triple t) {
     return t;
 }
 
+__device__ __forceinline__ float first_of(float x) { return bitsf((uint32_t)__builtin_amdgcn_readfirstlane((int)fbits(x))); }
+
 // An integer in the order of the values: at least 1, -0 as +0, NaN as -Inf
 __device__ __forceinline__ uint32_t order_of(float z) {
     const uint32_t u = fbits(z != z ? -INFINITY : z + 0.0f);
@@ -90,12 +92,61 @@ __device__ __forceinline__ float value_of(uint32_t o) { return bitsf((o >> 31) ?
 // larger values first, then lower places
 __device__ __forceinline__ uint64_t key_of(uint32_t order, uint32_t place) { return (uint64_t)order << 32 | (uint32_t)~place; }
 
+// the largest of a wave's numbers, in lane 63, by lane moves in the vector unit
+__device__ __forceinline__ uint32_t wave_max(uint32_t v) {
+#define MOVED(ctrl, rows) v = max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, ctrl, rows, 0xf, false))
+    MOVED(0x111, 0xf);                                // by 1, 2, 4, 8 lanes of a row of 16
+    MOVED(0x112, 0xf);
+    MOVED(0x114, 0xf);
+    MOVED(0x118, 0xf);
+    MOVED(0x142, 0xa);                                // a row's last to the next row, then half a wave's
+    MOVED(0x143, 0xc);
+#undef MOVED
+    return (uint32_t)__builtin_amdgcn_readlane((int)v, 63);
+}
+// Bisection: from `lo` up, the largest value that at least k of the numbers (N
+// a lane, the same in every wave) reach, or one that no more than `enough` do.
+// `lo` itself if fewer than k reach it.  All of them reach the smallest.
+template <int N>
+__device__ __forceinline__ int reach(const uint32_t (&of)[N], uint32_t b) {
+    int n = 0;
+#pragma unroll
+    for (int i = 0; i < N; i++) n += __popcll(__ballot(of[i] >= b));
+    return n;
+}
+template <int N>
+__device__ __forceinline__ uint32_t narrow(const uint32_t (&of)[N], uint32_t lo, int k, int enough) {
+    uint32_t most = of[0], least = of[0];
+#pragma unroll
+    for (int i = 1; i < N; i++) {
+        most = max(most, of[i]);
+        least = min(least, of[i]);
+    }
+    uint32_t hi = wave_max(most) + 1;                 // which none reaches; no order is 2^32 - 1
+    lo = max(lo, ~wave_max(~least));
+    while (hi - lo > 1) {
+        const uint32_t mid = lo + (hi - lo) / 2;
+        const int n = reach(of, mid);
+        if (n >= k) {
+            lo = mid;
+            if (n <= enough) break;
+        } else {
+            hi = mid;
+        }
+    }
+    return lo;
+}
+// a few more than k: each step of the bisection costs as much as ranking some
+__device__ __forceinline__ int few_more(int k) { return k + k / 2 + 4; }
+
 // Writes the k largest of n distinct keys in order.
 __device__ __forceinline__ void rank_keys(const uint64_t* keys, int n, uint64_t* best, int k, int tid) {
     for (int i = tid; i < n; i += LT) {
         const uint64_t mine = keys[i];
         int r = 0;
-        for (int j = 0; j < n; j++) r += keys[j] > mine;
+        int j = 0;
+        for (; j + 4 <= n; j += 4) r += (keys[j] > mine) + (keys[j + 1] > mine) + (keys[j + 2] > mine) + (keys[j + 3] > mine);
+        for (; j < n; j++) r += keys[j] > mine;
         if (r < k) best[r] = mine;
     }
 }
@@ -188,28 +239,8 @@ __global__ __launch_bounds__(LT) void k_logprobs(LogprobParams p) {
             uint32_t of[LT / 64];
 #pragma unroll
             for (int i = 0; i < LT / 64; i++) of[i] = lane_max[64 * i + lane];
-            auto reach = [&](uint32_t b) {
-                int n = 0;
-#pragma unroll
-                for (int i = 0; i < LT / 64; i++) n += __popcll(__ballot(of[i] >= b));
-                return n;
-            };
-            if (reach(beat + 1)) {
-                // the largest b that at least k lanes reach, or one that not many more do
-                uint32_t lo = beat + 1, hi = 0xffffffffu;      // k lanes reach lo or lo is the least; hi is reached by fewer
-                auto narrow = [&](int enough) {
-                    while (hi - lo > 1) {
-                        const uint32_t mid = lo + (hi - lo) / 2;
-                        const int n = reach(mid);
-                        if (n >= k) {
-                            lo = mid;
-                            if (n <= enough) break;
-                        } else {
-                            hi = mid;
-                        }
-                    }
-                };
-                narrow(k + k / 2 + 4);
+            if (reach(of, beat + 1)) {
+                uint32_t lo = narrow(of, beat + 1, k, few_more(k));
                 auto gather = [&](uint32_t least, int most) {  // keys of elements of at least `least`
                     const bool all = least <= LEAST;           // NaN too
                     const float z0 = all ? -INFINITY : value_of(least);
@@ -231,7 +262,7 @@ __global__ __launch_bounds__(LT) void k_logprobs(LogprobParams p) {
                     // Ties, mostly: the k-th largest itself, what lies above it (of
                     // fewer than k lanes), and of the elements equal to it the first
                     // k places.
-                    narrow(0);
+                    lo = narrow(of, lo, k, 0);
                     __syncthreads();
                     if (tid == 0) found = 0;
                     __syncthreads();
@@ -241,7 +272,6 @@ __global__ __launch_bounds__(LT) void k_logprobs(LogprobParams p) {
                     int ties = 0;
 #pragma unroll
                     for (int v = 0; v < NV; v++) {
-                        if (ties >= k) break;
                         uint32_t mask = 0;
 #pragma unroll
                         for (int e = 0; e < PER; e++)
@@ -303,15 +333,32 @@ __global__ __launch_bounds__(LT) void k_logprobs(LogprobParams p) {
     }
 }
 
-// Joins the splits of a row.
+// Joins the splits of a row.  A split's keys are in order (0 where it has fewer):
+// the ceil(k / j)-th largest of the splits' j-th keys has k keys that are no
+// smaller, and for j twice k / splits few more, so those are ranked alone.
 template <bool BF, bool TOP>
 __global__ __launch_bounds__(LT) void k_logprobs_join(LogprobParams p) {
     __shared__ uint64_t keys[TOP ? MOST_KEYS : 1], best[TOP ? MOST_TOP : 1];
+    __shared__ uint64_t least;
+    __shared__ int found;
     const int64_t t = blockIdx.x;
-    const int tid = threadIdx.x, k = p.top, n = p.splits * k;
-    const Triple* parts = reinterpret_cast<const Triple*>(p.parts) + t * p.splits;
+    const int tid = threadIdx.x, lane = tid & 63, k = p.top, splits = p.splits, n = splits * k;
+    constexpr int PER = TOP ? MOST_KEYS / LT : 1;
+    uint64_t mine[PER];
+    if constexpr (TOP) {
+#pragma unroll
+        for (int i = 0; i < PER; i++) mine[i] = tid + LT * i < n ? p.keys[t * n + tid + LT * i] : 0ull;
+        if (tid == 0) {
+            least = 1ull;                                      // no place without a key
+            found = 0;
+        }
+    }
+    const Triple* parts = reinterpret_cast<const Triple*>(p.parts) + t * splits;
     Triple s = {-INFINITY, 0.f, 0.f};
-    for (int i = 0; i < p.splits; i++) s = join(s, parts[i]);
+    for (int i = lane; i < splits; i += 64) s = join(s, parts[i]);
+    for (int o = 1; o < splits && o < 64; o <<= 1)
+        s = join(s, Triple{__shfl_xor(s.m, o, 64), __shfl_xor(s.s, o, 64), __shfl_xor(s.w, o, 64)});
+    s = Triple{first_of(s.m), first_of(s.s), first_of(s.w)};           // lanes from `splits` on joined nothing
     if (tid == 0) {
         const Row<BF> row(p.z, t, p.tokens, p.ld, p.vocab);
         const int64_t target = p.targets[t];
@@ -319,10 +366,27 @@ __global__ __launch_bounds__(LT) void k_logprobs_join(LogprobParams p) {
         finish(p, t, s, in ? row.one(target) : 0.f, in);
     }
     if constexpr (TOP) {
-        for (int i = tid; i < n; i += LT) keys[i] = p.keys[t * n + i];
+#pragma unroll
+        for (int i = 0; i < PER; i++)
+            if (tid + LT * i < n) keys[tid + LT * i] = mine[i];
         __syncthreads();
-        // places without a key rank behind every key, and there are k keys
-        rank_keys(keys, n, best, k, tid);
+        const int j = (2 * k + splits - 1) / splits < k ? (2 * k + splits - 1) / splits : k, m = (k + j - 1) / j;
+        for (int i = tid; i < splits; i += LT) {
+            const uint64_t it = keys[i * k + j - 1];
+            int r = 0;
+#pragma unroll 4
+            for (int x = 0; x < splits; x++) r += keys[x * k + j - 1] > it;
+            if (r == m - 1 && it) least = it;
+        }
+        __syncthreads();
+        const uint64_t bound = least;
+        // the few go to the front of the keys' place, which everyone has read
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < PER; i++)
+            if (mine[i] >= bound) keys[atomicAdd(&found, 1)] = mine[i];
+        __syncthreads();
+        rank_keys(keys, found, best, k, tid);
         __syncthreads();
         if (tid < k) put_top(p, t, tid, best[tid], s);
     }
@@ -398,10 +462,11 @@ hipError_t run(const LogprobParams& p, hipStream_t s) {
 
 }  // namespace
 
-// Segments a row is cut into (32 KB each, and one for an unaligned start), and how many a workgroup
-// takes: one while the launch does not fill the chip.
-LogprobPlan logprob_plan(int64_t tokens, int64_t vocab, int top, bool bf16) {
-    const int64_t size = LT * NV * (bf16 ? 8 : 4), segments = (vocab + (bf16 ? 7 : 3) + size - 1) / size;
+// Segments a row is cut into (16 KB each, an unaligned start included), and how
+// many a workgroup takes: one while the launch does not fill the chip.
+LogprobPlan logprob_plan(int64_t tokens, int64_t vocab, int64_t ld, int top, bool bf16) {
+    const int per = bf16 ? 8 : 4, unaligned = tokens > 1 && ld % per ? per - 1 : 0;
+    const int64_t size = LT * NV * per, segments = (vocab + unaligned + size - 1) / size;
     LogprobPlan o;
     int64_t splits = tokens >= 1024 ? 1 : 2048 / tokens;
     if (splits > segments) splits = segments;
