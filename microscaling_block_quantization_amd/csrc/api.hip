@@ -928,7 +928,7 @@ int mx_attend_shared(const mx_kv_cache* cache, const mx_heads* q, int64_t batch,
 
 size_t mx_lora_workspace_size(const mx_adapters* a, int64_t tokens) {
     if (check_adapters(a) || tokens <= 0 || tokens > MAX_LORA_TOKENS) return 0;
-    return round_up((size_t)mxk::lora_rows(tokens) * a->rank * sizeof(float));
+    return round_up((size_t)mxk::lora_bytes(tokens, a->rank));
 }
 
 int mx_lora(const mx_adapters* a, const void* x, int64_t tokens, int64_t ldx, const int32_t* ids, int base_dtype,

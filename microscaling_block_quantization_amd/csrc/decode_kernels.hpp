@@ -155,11 +155,11 @@ struct LoraParams {
     void* y;
     int64_t ldy;
     int base_bf16, y_bf16, vec_base, vec_y;      // vec: rows start at multiples of 16 bytes
-    float* h;                      // [split][token][rank]
-    int splits, spread, rank_groups, run;        // set by the launcher
+    float* h;                      // [split][token][rank], or `thirds`: bf16 [token][part][rank]
+    int thirds, splits, spread, rank_groups, run;        // set by the launcher
 };
-// Rows of h, at most, of any call of at most this many tokens
-int64_t lora_rows(int64_t tokens);
+// Bytes of h, at most, of any call of at most this many tokens
+int64_t lora_bytes(int64_t tokens, int64_t rank);
 hipError_t launch_lora(LoraParams p, hipStream_t s);
 
 constexpr int MOST_TOP = 64;       // alternatives of a row

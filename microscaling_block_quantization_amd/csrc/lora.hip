@@ -35,6 +35,11 @@ __device__ __forceinline__ Ids tile_ids(const LoraParams& p, int64_t t0, int c) 
     Ids o;
     o.id = t0 + c < p.tokens ? p.ids[t0 + c] : -1;
     if (o.id < 0 || o.id >= p.count) o.id = -1;
+    const int id0 = __builtin_amdgcn_readfirstlane(o.id);
+    if (__all(o.id == id0)) {                         // a prompt's tile
+        o.first = id0 >= 0 ? 1u : 0u;
+        return o;
+    }
     bool again = o.id < 0;
 #pragma unroll
     for (int i = 0; i < TOK - 1; i++) again |= i < c && __builtin_amdgcn_readlane(o.id, i) == o.id;
@@ -64,7 +69,8 @@ __device__ __forceinline__ f4v mfma_f32(u32x4 a, u32x4 b, f4v c) {
 // ---------------------------------------------------------------------------
 // h = A x.  Eight waves share K in steps of 64 bytes a lane, RT tiles of 16
 // ranks each; a workgroup takes one of `splits` runs of K.  The waves' sums are
-// added in LDS in their order, the runs' by the second product.
+// added in LDS in their order and scaled, the runs' by the second product.  More
+// than 16 tokens have one run, and their bf16 parts are formed here, once.
 // ---------------------------------------------------------------------------
 constexpr int SW = 8;
 
@@ -140,7 +146,14 @@ __global__ __launch_bounds__(64 * SW) void k_lora_down(LoraParams p) {
         float v = 0.f;
 #pragma unroll
         for (int q = 0; q < SW; q++) v += red[q][i / 16][t * 16 + i % 16];
-        p.h[((int64_t)split * p.tokens + t0 + t) * p.rank + r0 + i] = v;
+        if (p.scales) v *= p.scales[id];
+        if (!F32 && p.thirds) {
+            uint16_t* h = reinterpret_cast<uint16_t*>(p.h) + (t0 + t) * 3 * p.rank + r0 + i;
+#pragma unroll
+            for (int part = 0; part < 3; part++) h[part * p.rank] = part3(v, part);
+        } else {
+            p.h[((int64_t)split * p.tokens + t0 + t) * p.rank + r0 + i] = v;
+        }
     }
 }
 
@@ -151,44 +164,57 @@ __global__ __launch_bounds__(64 * SW) void k_lora_down(LoraParams p) {
 // ---------------------------------------------------------------------------
 constexpr int UW = 4;
 
+// N values of a token's row (4 or 16) as they lie in memory, and as numbers
 template <bool BF, int N>
-__device__ __forceinline__ void load_run(float (&o)[N], const void* p, int64_t at, int have, bool vec) {
-    if (BF) {
-        const uint16_t* x = static_cast<const uint16_t*>(p) + at;
+struct Run {
+    static constexpr int W = BF ? (N + 7) / 8 : N / 4;
+    u32x4 w[W];
+    __device__ __forceinline__ void load(const void* p, int64_t at, int have, bool vec) {
+        const char* x = static_cast<const char*>(p) + at * (BF ? 2 : 4);
         if (vec && have >= N) {
+            if constexpr (BF && N == 4) {
+                const uint2 v = *reinterpret_cast<const uint2*>(x);
+                w[0] = u32x4{v.x, v.y, 0u, 0u};
+            } else {
 #pragma unroll
-            for (int i = 0; i < N; i += 4) {
-                const uint2 w = *reinterpret_cast<const uint2*>(x + i);
-                o[i] = bf16lo(w.x); o[i + 1] = bf16hi(w.x); o[i + 2] = bf16lo(w.y); o[i + 3] = bf16hi(w.y);
+                for (int i = 0; i < W; i++) w[i] = *reinterpret_cast<const u32x4*>(x + 16 * i);
             }
         } else {
 #pragma unroll
-            for (int i = 0; i < N; i++) o[i] = i < have ? bf16f(x[i]) : 0.f;
-        }
-    } else {
-        const float* x = static_cast<const float*>(p) + at;
-        if (vec && have >= N) {
+            for (int i = 0; i < W; i++)
 #pragma unroll
-            for (int i = 0; i < N; i += 4) {
-                const f4v w = *reinterpret_cast<const f4v*>(x + i);
-                o[i] = w[0]; o[i + 1] = w[1]; o[i + 2] = w[2]; o[i + 3] = w[3];
-            }
-        } else {
-#pragma unroll
-            for (int i = 0; i < N; i++) o[i] = i < have ? x[i] : 0.f;
+                for (int e = 0; e < 4; e++) {
+                    uint32_t v = 0u;
+                    if constexpr (BF) {
+                        if (8 * i + 2 * e < have) v = reinterpret_cast<const uint16_t*>(x)[8 * i + 2 * e];
+                        if (8 * i + 2 * e + 1 < have) v |= (uint32_t)reinterpret_cast<const uint16_t*>(x)[8 * i + 2 * e + 1] << 16;
+                    } else {
+                        if (4 * i + e < have) v = reinterpret_cast<const uint32_t*>(x)[4 * i + e];
+                    }
+                    w[i][e] = v;
+                }
         }
     }
-}
+    __device__ __forceinline__ float value(int i) const {
+        if constexpr (BF) return (i & 1) ? bf16hi(w[i / 8][i / 2 % 4]) : bf16lo(w[i / 8][i / 2 % 4]);
+        else return bitsf(w[i / 4][i % 4]);
+    }
+};
 template <int N>
 __device__ __forceinline__ void store_run(const float (&o)[N], void* p, int64_t at, int have, bool vec, bool bf) {
     if (bf) {
         uint16_t* x = static_cast<uint16_t*>(p) + at;
         if (vec && have >= N) {
 #pragma unroll
-            for (int i = 0; i < N; i += 4) {
-                const f2v a = {o[i], o[i + 1]}, b = {o[i + 2], o[i + 3]};
-                *reinterpret_cast<uint2*>(x + i) = make_uint2(__builtin_bit_cast(uint32_t, __builtin_convertvector(a, bf2v)),
-                                                              __builtin_bit_cast(uint32_t, __builtin_convertvector(b, bf2v)));
+            for (int i = 0; i < N; i += N < 8 ? 4 : 8) {
+                uint32_t w[4];
+#pragma unroll
+                for (int e = 0; e < (N < 8 ? 2 : 4); e++) {
+                    const f2v a = {o[i + 2 * e], o[i + 2 * e + 1]};
+                    w[e] = __builtin_bit_cast(uint32_t, __builtin_convertvector(a, bf2v));
+                }
+                if constexpr (N < 8) *reinterpret_cast<uint2*>(x + i) = make_uint2(w[0], w[1]);
+                else *reinterpret_cast<u32x4*>(x + i) = u32x4{w[0], w[1], w[2], w[3]};
             }
         } else {
 #pragma unroll
@@ -209,7 +235,7 @@ __device__ __forceinline__ void store_run(const float (&o)[N], void* p, int64_t 
 }
 
 // R8: runs of 8 ranks of a group (1, 2, 4 or 8), further groups of 64 in turn
-template <bool F32, int R8, int NT>
+template <bool F32, int R8, int NT, bool BB>
 __global__ __launch_bounds__(64 * UW) void k_lora_up(LoraParams p) {
     constexpr int ES = F32 ? 4 : 2, N = 4 * NT;
     // bf16: K slot 8 (4 j + g) holds run (4 j + g) % R8 of part (4 j + g) / R8;
@@ -226,10 +252,11 @@ __global__ __launch_bounds__(64 * UW) void k_lora_up(LoraParams p) {
     const int have = (int)(p.n - n < N ? p.n - n : N);                   // may be negative
     const int groups = (p.rank + 8 * R8 - 1) / (8 * R8);
 
-    u32x4 w[NT][FR];
-    int held = -1;
     // B's rows of group q: row i of tile s is output n0 + N (i / 4) + 4 s + i % 4
-    auto load_b = [&](int a, int q) {
+    struct Rows {
+        u32x4 w[NT][FR];
+    };
+    auto load_b = [&](Rows& o, int a, int q) {
 #pragma unroll
         for (int s = 0; s < NT; s++) {
             const int64_t row = n0 + N * (c / 4) + 4 * s + c % 4;
@@ -237,70 +264,104 @@ __global__ __launch_bounds__(64 * UW) void k_lora_up(LoraParams p) {
 #pragma unroll
             for (int f = 0; f < FR; f++) {
                 const int r = q * 8 * R8 + (F32 ? 16 * f + 4 * g : R8 <= 4 ? 8 * (g % R8) : 32 * f + 8 * g);
-                w[s][f] = r < p.rank ? *reinterpret_cast<const u32x4*>(b + r * ES) : u32x4{0u, 0u, 0u, 0u};
+                o.w[s][f] = r < p.rank ? *reinterpret_cast<const u32x4*>(b + r * ES) : u32x4{0u, 0u, 0u, 0u};
             }
         }
     };
-    for (int64_t tile = first; tile < last; tile++) {
-        const int64_t t0 = tile * TOK, tok = t0 + c < p.tokens ? t0 + c : p.tokens - 1;
-        const Ids ids = tile_ids(p, t0, c);
-        float base[N];
-        if (p.base) {
-            if (p.base_bf16) load_run<true>(base, p.base, tok * p.ld_base + n, have, p.vec_base);
-            else load_run<false>(base, p.base, tok * p.ld_base + n, have, p.vec_base);
-        } else {
+    // What a tile of tokens brings along, loaded a tile ahead.  h of a token
+    // without an adapter is whatever the workspace held, and masked.
+    constexpr bool THIRDS = !F32 && NT > 1;                              // h comes in its bf16 parts
+    constexpr int V = F32 ? 4 : 8, HV = THIRDS ? 1 : V / 4;
+    struct Tokens {
+        Ids ids;
+        Run<BB, N> base;
+        f4v h[J][HV];
+    };
+    auto load_h = [&](f4v (&h)[J][HV], int64_t tok, int q) {
 #pragma unroll
-            for (int i = 0; i < N; i++) base[i] = 0.f;
+        for (int j = 0; j < J; j++) {
+            const int slot = 4 * j + g, r = q * 8 * R8 + (F32 ? 4 * slot : 8 * (slot % R8));
+            const bool in = (F32 || slot < 3 * R8) && r < p.rank;
+#pragma unroll
+            for (int e = 0; e < HV; e++) h[j][e] = f4v{0.f, 0.f, 0.f, 0.f};
+            if constexpr (THIRDS) {
+                const uint16_t* from = reinterpret_cast<const uint16_t*>(p.h) + (tok * 3 + slot / R8) * p.rank + r;
+                if (in) h[j][0] = *reinterpret_cast<const f4v*>(from);
+                continue;
+            }
+            for (int s = 0; in && s < p.splits; s++) {
+                const f4v* from = reinterpret_cast<const f4v*>(p.h + ((int64_t)s * p.tokens + tok) * p.rank + r);
+#pragma unroll
+                for (int e = 0; e < HV; e++) h[j][e] = s ? h[j][e] + from[e] : from[e];
+            }
         }
+    };
+    auto token_of = [&](int64_t tile) { return tile * TOK + c < p.tokens ? tile * TOK + c : p.tokens - 1; };
+    auto load_tokens = [&](Tokens& o, int64_t tile) {
+        const int64_t tok = token_of(tile);
+        o.ids = tile_ids(p, tile * TOK, c);
+        // without a base: nothing is there to load, and zeros are loaded
+        o.base.load(p.base, tok * p.ld_base + n, p.base ? have : 0, p.vec_base);
+        load_h(o.h, tok, 0);
+    };
+    // adapters whose rows are asked for at once: a decode tile names many
+    constexpr int AT = NT == 1 && R8 <= 4 ? 4 : 1;
+    Rows w[AT];
+    int held = -1;
+    Tokens now, next;
+    load_tokens(now, first);
+    for (int64_t tile = first; tile < last; tile++) {
+        if (tile + 1 < last) load_tokens(next, tile + 1);
         f4v acc[NT];
 #pragma unroll
         for (int s = 0; s < NT; s++) acc[s] = f4v{0.f, 0.f, 0.f, 0.f};
-        const float scale = p.scales && ids.id >= 0 ? p.scales[ids.id] : 1.f;
         for (int q = 0; q < groups; q++) {
+            if (q) load_h(now.h, token_of(tile), q);
             // the token's h as columns
             u32x4 h[J];
 #pragma unroll
-            for (int j = 0; j < J; j++) {
-                const int slot = 4 * j + g, part = F32 ? 0 : slot / R8;
-                const int r = q * 8 * R8 + (F32 ? 4 * slot : 8 * (slot % R8));
-                constexpr int V = F32 ? 4 : 8;
-                float v[V];
-#pragma unroll
-                for (int e = 0; e < V; e++) v[e] = 0.f;
-                if (ids.id >= 0 && part < 3 && r < p.rank)
-                    for (int s = 0; s < p.splits; s++) {
-                        const f4v* from = reinterpret_cast<const f4v*>(p.h + ((int64_t)s * p.tokens + tok) * p.rank + r);
-#pragma unroll
-                        for (int e = 0; e < V; e++) v[e] += from[e / 4][e % 4];
-                    }
+            for (int j = 0; j < J; j++)
 #pragma unroll
                 for (int e = 0; e < 4; e++) {
-                    if (F32) h[j][e] = fbits(v[e] * scale);
-                    else h[j][e] = part3(v[(2 * e) % V] * scale, part) | (uint32_t)part3(v[(2 * e + 1) % V] * scale, part) << 16;
+                    if constexpr (F32 || THIRDS) {
+                        h[j][e] = fbits(now.h[j][0][e]);
+                    } else {
+                        const int part = (4 * j + g) / R8;
+                        const f4v v = now.h[j][e / 2 % HV];
+                        h[j][e] = part < 3 ? part3(v[2 * e % 4], part) | (uint32_t)part3(v[(2 * e + 1) % 4], part) << 16 : 0u;
+                    }
                 }
-            }
-            for (uint32_t left = ids.first; left; left &= left - 1) {
-                const int a = __builtin_amdgcn_readlane(ids.id, __builtin_ctz(left));
-                if (a != held || groups > 1) {
-                    load_b(a, q);
-                    held = a;
+            for (uint32_t left = now.ids.first; left;) {
+                int a[AT];
+#pragma unroll
+                for (int i = 0; i < AT; i++) {                           // -2: no further one
+                    a[i] = left ? __builtin_amdgcn_readlane(now.ids.id, __builtin_ctz(left)) : -2;
+                    left = left ? left & (left - 1) : 0u;
+                    if (a[i] >= 0 && (AT > 1 || a[i] != held || groups > 1)) load_b(w[i], a[i], q);
                 }
+                held = a[0];
 #pragma unroll
-                for (int j = 0; j < J; j++) {
-                    const u32x4 x = ids.id == a ? h[j] : u32x4{0u, 0u, 0u, 0u};
+                for (int i = 0; i < AT; i++) {
+                    if (a[i] < 0) break;
 #pragma unroll
-                    for (int s = 0; s < NT; s++) {
-                        if (F32) acc[s] = mfma_f32(w[s][j % FR], x, acc[s]);
-                        else acc[s] = mfma_bf16(w[s][j % FR], x, acc[s]);
+                    for (int j = 0; j < J; j++) {
+                        const u32x4 x = now.ids.id == a[i] ? h[j] : u32x4{0u, 0u, 0u, 0u};
+#pragma unroll
+                        for (int s = 0; s < NT; s++) {
+                            if (F32) acc[s] = mfma_f32(w[i].w[s][j % FR], x, acc[s]);
+                            else acc[s] = mfma_bf16(w[i].w[s][j % FR], x, acc[s]);
+                        }
                     }
                 }
             }
         }
-        if (t0 + c < p.tokens && have > 0) {
+        if (tile * TOK + c < p.tokens && have > 0) {
+            float y[N];
 #pragma unroll
-            for (int i = 0; i < N; i++) base[i] += acc[i / 4][i % 4];
-            store_run(base, p.y, tok * p.ldy + n, have, p.vec_y, p.y_bf16);
+            for (int i = 0; i < N; i++) y[i] = now.base.value(i) + acc[i / 4][i % 4];
+            store_run(y, p.y, token_of(tile) * p.ldy + n, have, p.vec_y, p.y_bf16);
         }
+        now = next;
     }
 }
 
@@ -315,7 +376,8 @@ template <bool F32, int R8, int NT>
 hipError_t up(const LoraParams& p, hipStream_t s) {
     const int64_t n = (p.n + 16 * NT * UW - 1) / (16 * NT * UW), tiles = (p.tokens + TOK - 1) / TOK;
     const dim3 grid((unsigned)n, (unsigned)((tiles + p.run - 1) / p.run));
-    k_lora_up<F32, R8, NT><<<grid, 64 * UW, 0, s>>>(p);
+    if (p.base_bf16) k_lora_up<F32, R8, NT, true><<<grid, 64 * UW, 0, s>>>(p);
+    else k_lora_up<F32, R8, NT, false><<<grid, 64 * UW, 0, s>>>(p);
     return hipGetLastError();
 }
 template <bool F32, int NT>
@@ -335,20 +397,22 @@ hipError_t both(LoraParams p, hipStream_t s) {
 }  // namespace
 
 // Runs of K for few tokens, whose first product is a chain of loads
-constexpr int FEW = 64, MOST_SPLITS = 8;
+constexpr int MOST_SPLITS = 8;
 int lora_splits(int64_t tokens, int64_t k) {
-    if (tokens > FEW) return 1;
+    if (tokens > TOK) return 1;
     const int64_t n = k / 1024;
     return (int)(n < 1 ? 1 : n > MOST_SPLITS ? MOST_SPLITS : n);
 }
-int64_t lora_rows(int64_t tokens) {
-    const int64_t few = (tokens < FEW ? tokens : FEW) * MOST_SPLITS;
-    return tokens > few ? tokens : few;
+// three bf16 parts, or an fp32 for each run, of each token
+int64_t lora_bytes(int64_t tokens, int64_t rank) {
+    const int64_t few = (tokens < TOK ? tokens : TOK) * MOST_SPLITS * 4, many = tokens * 6;
+    return (few > many ? few : many) * rank;
 }
 
 hipError_t launch_lora(LoraParams p, hipStream_t s) {
     const int64_t tiles = (p.tokens + TOK - 1) / TOK;
     p.splits = lora_splits(p.tokens, p.k);
+    p.thirds = p.bf16 && p.tokens > TOK;
     p.spread = p.tokens <= 1024 ? (int)(p.tokens < TOK ? p.tokens : TOK) : 1;
     if (p.spread > p.count) p.spread = p.count > 0 ? p.count : 1;
     // tiles of tokens a workgroup goes down: about 2048 workgroups
