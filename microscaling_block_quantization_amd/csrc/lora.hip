@@ -67,7 +67,7 @@ __device__ __forceinline__ f4v mfma_f32(u32x4 a, u32x4 b, f4v c) {
 }
 
 // ---------------------------------------------------------------------------
-// h = A x.  Eight waves share K in steps of 64 bytes a lane, RT tiles of 16
+// h = A x.  Eight waves share K in steps of 256 bytes, RT tiles of 16
 // ranks each; a workgroup takes one of `splits` runs of K.  The waves' sums are
 // added in LDS in their order and scaled, the runs' by the second product.  More
 // than 16 tokens have one run, and their bf16 parts are formed here, once.
@@ -76,7 +76,7 @@ constexpr int SW = 8;
 
 template <bool F32, int RT>
 __global__ __launch_bounds__(64 * SW) void k_lora_down(LoraParams p) {
-    constexpr int ES = F32 ? 4 : 2, PER = 64 / ES, STEP = 4 * PER;       // values a lane and a wave take at a time
+    constexpr int ES = F32 ? 4 : 2, STEP = 256 / ES;                     // values a wave takes at a time
     __shared__ __attribute__((aligned(16))) float red[SW][RT][256];
     const int tid = threadIdx.x, lane = tid & 63, c = lane & 15, g = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -91,7 +91,7 @@ __global__ __launch_bounds__(64 * SW) void k_lora_down(LoraParams p) {
     const int k = (int)p.k, steps = (k + STEP - 1) / STEP;
     const int from = (int)((int64_t)split * steps / p.splits), to = (int)((int64_t)(split + 1) * steps / p.splits);
     const int64_t tok = t0 + c < p.tokens ? t0 + c : p.tokens - 1;
-    const char* x = static_cast<const char*>(p.x) + (tok * p.ldx + PER * g) * ES;
+    const char* x = static_cast<const char*>(p.x) + tok * p.ldx * ES + 16 * g;
 
     f4v acc[RT];
 #pragma unroll
@@ -104,21 +104,21 @@ __global__ __launch_bounds__(64 * SW) void k_lora_down(LoraParams p) {
 #pragma unroll
         for (int i = 0; i < RT; i++) {
             const int r = r0 + 16 * i + c < p.rank ? r0 + 16 * i + c : p.rank - 1;
-            w[i] = static_cast<const char*>(p.a) + (((int64_t)a * p.rank + r) * k + PER * g) * ES;
+            w[i] = static_cast<const char*>(p.a) + ((int64_t)a * p.rank + r) * k * ES + 16 * g;
         }
         f4v sum[RT];
 #pragma unroll
         for (int i = 0; i < RT; i++) sum[i] = f4v{0.f, 0.f, 0.f, 0.f};
         for (int s = from + wave; s < to; s += SW) {
-            const int k0 = s * STEP, have = (k - k0 - PER * g) * ES / 16;      // 16-byte pieces of this lane's that exist
+            const int at = s * STEP * ES;                                // bytes; four lanes take 64 of a row at once
             u32x4 xv[4], wv[RT][4];
 #pragma unroll
             for (int j = 0; j < 4; j++) {
-                const bool in = j < have;
-                xv[j] = in ? *reinterpret_cast<const u32x4*>(x + (int64_t)k0 * ES + 16 * j) : u32x4{0u, 0u, 0u, 0u};
+                const bool in = at + 64 * j + 16 * g < k * ES;
+                xv[j] = in ? *reinterpret_cast<const u32x4*>(x + at + 64 * j) : u32x4{0u, 0u, 0u, 0u};
 #pragma unroll
                 for (int i = 0; i < RT; i++)
-                    wv[i][j] = in ? *reinterpret_cast<const u32x4*>(w[i] + (int64_t)k0 * ES + 16 * j) : u32x4{0u, 0u, 0u, 0u};
+                    wv[i][j] = in ? *reinterpret_cast<const u32x4*>(w[i] + at + 64 * j) : u32x4{0u, 0u, 0u, 0u};
             }
 #pragma unroll
             for (int j = 0; j < 4; j++)
