@@ -462,8 +462,9 @@ int mx_cache_read(const mx_kv_cache *cache, const int64_t *slots, int64_t tokens
  * prefix_table[t / page_size], and then over the sequence's own, t <
  * lengths[b] by page_table and lengths as in mx_attend.  The result is
  * mx_attend's for the prefix's and the own tokens as one sequence; the prefix
- * is read once for all sequences (for up to 128 pairs of a sequence and a query
- * head of one key-value head, and once more for each further 128).
+ * is read once for all sequences (for up to 256 pairs of a sequence and a query
+ * head of one key-value head, 128 with fp32 queries or more than 128 values a
+ * head, and once more for each further as many).
  *  - prefix_table, prefix_length (one number): int32 on the device.
  *    *prefix_length <= 0 is no prefix, one past the table counts as the table.
  *    lengths[b] <= 0: the prefix alone.  Neither: out 0, lse -inf.  A page

@@ -966,18 +966,18 @@ def mx_logprobs(logits, targets, top=0, workspace=None, stream=None):
     tokens, vocab, ld, at = _logits(logits, targets, "mx_logprobs")
     if not 0 <= top <= min(64, vocab):
         raise ValueError(f"mx_logprobs: top must be 0 .. {min(64, vocab)}")
-    made = logits.new_empty((3 + top, tokens), dtype=torch.float32)
-    logprob, lse, entropy = made[:3]
+    made = logits.new_empty((3, tokens), dtype=torch.float32)
+    logprob, lse, entropy = made.unbind(0)
     tops = ids = None
     if top:
-        tops, ids = made[3:].view(tokens, top), logits.new_empty((tokens, top), dtype=torch.int64)
+        tops, ids = logits.new_empty((tokens, top), dtype=torch.float32), logits.new_empty((tokens, top), dtype=torch.int64)
     if workspace is None:
         workspace = logits.new_empty((lib().mx_logprobs_workspace_size(tokens, vocab, top),), dtype=torch.uint8)
     elif workspace.get_device() != dev or not workspace.is_contiguous():
         _buffer(workspace, 0, dev, "mx_logprobs", "workspace")
     p = made.data_ptr()
     _check(lib().mx_logprobs(_code(logits.dtype), logits.data_ptr(), tokens, vocab, ld, at, p, p + 4 * tokens, p + 8 * tokens, top,
-                             p + 12 * tokens if top else 0, _raw(ids), workspace.data_ptr(), workspace.nbytes,
+                             _raw(tops), _raw(ids), workspace.data_ptr(), workspace.nbytes,
                              _stream_ptr(dev, "mx_logprobs")), "mx_logprobs")
     return (logprob, lse, entropy, tops, ids) if top else (logprob, lse, entropy)
 
