@@ -12,6 +12,14 @@
 // below, and few elements besides the k largest reach it, so those are gathered
 // in LDS and ranked by counting.  The bound is found by bisection over the
 // values' order-preserving integers, each step four ballots.
+//
+// Bound and measured.  Large launches: memory; the gradient of 4096 x 131072 bf16
+// 372 us, 5.8 TB/s read and written, of 333 x 50001 fp32 (rows at every
+// alignment) 21 us.  64 rows of 131072 bf16 with 20 alternatives: 14.2 us and 4.6
+// for the join, one round of workgroups whose load, exponentials, bisection and
+// ranking follow each other.  Segments of 32 KB there 26 us, bisection over all
+// integers instead of the lanes' range 15.2; the join by ranking every key 6.5,
+// by bisection 8.8, by binary search in the splits' lists 14.5.
 #include "decode_kernels.hpp"
 
 namespace mxk {

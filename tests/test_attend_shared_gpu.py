@@ -290,3 +290,35 @@ def test_offsets_past_32_bits():
     check(small, torch.tensor([1, 0]), pn, table, none, q, dim ** -0.5, out, lse, "far pages")
     rk, rv = mx.mx_cache_read(cache, slots)
     assert torch.equal(rk, kv[:, :heads]) and torch.equal(rv, kv[:, heads:])
+
+
+@pytest.mark.parametrize("kind,heads,batch,group,prefix,same", [("bf16", 8, 75, 4, 40000, True), ("mxfp8", 64, 3, 1, 6000, False),
+                                                                ("mxfp4", 32, 20, 4, 12000, True)])
+def test_ranges_of_many_pages(kind, heads, batch, group, prefix, same):
+    """Pages of one token: a range has more of them than are held at a time.  The
+    same tokens on pages of 64 give the same bits where a tile of 32 or 64 tokens
+    ends with them, and the same values elsewhere."""
+    g = torch.Generator(device="cuda").manual_seed(heads)
+    kv = torch.randn(prefix, 2 * heads, 64, generator=g, device="cuda").to(BF16)
+    q = torch.randn(batch, heads * group, 64, generator=g, device="cuda").to(BF16)
+    got = []
+    for page in (1, 64):
+        pages = -(-prefix // page)
+        cache = mx.alloc_kv_cache(FORMATS[kind], pages, page, heads, 64)
+        ahead = torch.randperm(pages, generator=g, device="cuda").to(torch.int32)
+        t = torch.arange(prefix, device="cuda")
+        mx.mx_cache_write(cache, kv[:, :heads], kv[:, heads:], ahead[t // page].long() * page + t % page)
+        none = torch.zeros(batch, dtype=torch.int32, device="cuda")
+        got.append(call(cache, ahead, torch.tensor([prefix], dtype=torch.int32, device="cuda"), none[:, None].contiguous(), none, q))
+    (a, la), (b, lb) = got
+    if same:
+        assert torch.equal(a, b) and torch.equal(la, lb)
+    assert (a.float() - b.float()).abs().max() <= 2.0 ** -7 * b.float().abs().max() and (la - lb).abs().max() < 1e-5
+    # against the definition: the first and the last sequence
+    for r in (0, batch - 1):
+        for h in (0, heads * group - 1):
+            z = torch.mv(kv[:, h // group].double(), q[r, h].double()) * 64 ** -0.5 if kind == "bf16" else None
+            if z is not None:
+                w = torch.mv(kv[:, heads + h // group].double().t().contiguous(), torch.softmax(z, 0))
+                assert (a[r, h].double() - w).abs().max() < 2.0 ** -7 * w.abs().max()
+                assert abs(la[r, h].double() - torch.logsumexp(z, 0)) < 1e-4
