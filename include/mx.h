@@ -455,7 +455,11 @@ int mx_cache_read(const mx_kv_cache *cache, const int64_t *slots, int64_t tokens
                   const mx_heads *v, void *stream);
 
 /* ---- many requests on one base model ----------------------------------------
- * A batch whose requests share the quantized model and a prompt.             */
+ * A batch whose requests share the quantized model and a prompt.  Index vectors
+ * (prefix and page tables, lengths, ids, targets, top_ids) and vectors of fp32
+ * per token or adapter (lse, logprob, entropy and their gradients,
+ * top_logprobs, scales) need the alignment of their elements alone.  A call
+ * whose launch would hold 2^32 threads or more is refused (MX_ERR_ARG).      */
 
 /* mx_attend for sequences that share their first tokens: sequence b and query
  * head h attend over the prefix's tokens, t < *prefix_length at

@@ -541,7 +541,7 @@ template <int D, int KIND, bool QF32, int RW, bool ONE>
 hipError_t go(const SharedParams& p, hipStream_t s) {
     constexpr int W = waves_of(D, QF32, ONE), lds = lds_bytes(D, W, RW);
     static_assert(lds + 8 * TABLE + 64 <= 160 * 1024, "LDS of a CU");
-    if (lds > 64 * 1024) {
+    if (lds + 8 * TABLE + 64 > 64 * 1024) {
         const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(k_prefix<D, KIND, QF32, RW, ONE>),
                                                  hipFuncAttributeMaxDynamicSharedMemorySize, lds);
         if (e != hipSuccess) return e;
