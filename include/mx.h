@@ -508,7 +508,8 @@ typedef struct mx_adapters {
  *    a row that name them, so tokens of one adapter are best side by side.
  *  - Products and sums are fp32 (a x too: bf16 operands enter exactly, and the
  *    rank values enter the second product as exact sums of three bf16 parts,
- *    multiples of 2^-133).  A NaN or Inf in a token's x reaches its y alone.
+ *    multiples of 2^-133).  A NaN or Inf in a token's x reaches its y alone,
+ *    one in an adapter the tokens that name it.
  *  - workspace: at least mx_lora_workspace_size(a, tokens) bytes, which serves
  *    fewer tokens and smaller ranks too; no initial contents needed; calls that
  *    share one must not overlap.  tokens <= 2^24.                             */

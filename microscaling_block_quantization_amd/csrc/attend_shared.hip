@@ -51,12 +51,9 @@ constexpr int lds_bytes(int D, int waves, int rw) {
     return rw == waves || tiles > join ? tiles : join;
 }
 
-// Left to itself the scheduler moves reads of LDS to right before their use.
-#define PHASE __builtin_amdgcn_sched_barrier(0)
-
 // One tile of RW x 32 rows and one range of the prefix's tokens.
 //
-// RW waves of a group stand along the rows, 4 / RW along the tokens.  The
+// RW of the W waves stand along the rows, W / RW along the tokens.  The
 // 32 x 32 x 16 instruction takes tokens as rows and query rows as columns, so a
 // lane holds 16 scores of one query row and the row's maximum is a maximum over
 // registers and one exchange; the scores' layout is the column operand of the
@@ -420,8 +417,6 @@ __global__ __launch_bounds__(64 * waves_of(D, QF32, ONE), waves_of(D, QF32, ONE)
         }
     }
 }
-#undef PHASE
-
 // Joins the parts of one sequence and query head, those of the prefix and those
 // of its own tokens: groups of D / 4 lanes (a power of two of them) take every
 // JG-th part, four values a lane, then their triples are joined in order.

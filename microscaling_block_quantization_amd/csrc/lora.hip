@@ -5,7 +5,7 @@
 // and B h.  Tokens come in tiles of 16, the columns of the 16 x 16 matrix
 // instruction, whose rows are ranks (first product) or outputs (second).
 // Columns are independent, so a tile whose tokens name several adapters runs
-// once for each distinct one, the others' columns masked: a decode batch costs
+// once for each distinct one and keeps its own columns: a decode batch costs
 // every adapter it uses once, a prompt of one adapter no more than a dense
 // product, and tokens need no sorting.  bf16 operands: the 16 x 16 x 32 bf16
 // instruction, h (fp32) as the exact sum of three bf16 parts side by side
@@ -276,7 +276,7 @@ __global__ __launch_bounds__(64 * UW) void k_lora_up(LoraParams p) {
         }
     };
     // What a tile of tokens brings along, loaded a tile ahead.  h of a token
-    // without an adapter is whatever the workspace held, and masked.
+    // without an adapter is whatever the workspace held, and not kept.
     constexpr bool THIRDS = !F32 && NT > 1;                              // h comes in its bf16 parts
     constexpr int V = F32 ? 4 : 8, HV = THIRDS ? 1 : V / 4;
     struct Tokens {
@@ -350,14 +350,17 @@ __global__ __launch_bounds__(64 * UW) void k_lora_up(LoraParams p) {
 #pragma unroll
                 for (int i = 0; i < AT; i++) {
                     if (a[i] < 0) break;
+                    // of its own tokens alone, by selection: what another adapter's
+                    // weights hold, a NaN say, reaches nobody else
 #pragma unroll
-                    for (int j = 0; j < J; j++) {
-                        const u32x4 x = now.ids.id == a[i] ? h[j] : u32x4{0u, 0u, 0u, 0u};
+                    for (int s = 0; s < NT; s++) {
+                        f4v sum = acc[s];
 #pragma unroll
-                        for (int s = 0; s < NT; s++) {
-                            if (F32) acc[s] = mfma_f32(w[i].w[s][j % FR], x, acc[s]);
-                            else acc[s] = mfma_bf16(w[i].w[s][j % FR], x, acc[s]);
+                        for (int j = 0; j < J; j++) {
+                            if (F32) sum = mfma_f32(w[i].w[s][j % FR], h[j], sum);
+                            else sum = mfma_bf16(w[i].w[s][j % FR], h[j], sum);
                         }
+                        if (now.ids.id == a[i]) acc[s] = sum;
                     }
                 }
             }

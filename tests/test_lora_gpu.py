@@ -125,6 +125,21 @@ def test_non_finite_tokens_stay_alone():
     assert torch.equal(y[keep], want[keep]) and y[4].isnan().all() and not y[9].isfinite().any()
 
 
+@pytest.mark.parametrize("tokens", [12, 40])
+@pytest.mark.parametrize("rank,dtype", [(8, BF16), (16, BF16), (72, BF16), (16, F32)])
+def test_non_finite_adapters_stay_alone(tokens, rank, dtype):
+    """NaN and Inf in an adapter's weights or scale reach the tokens that name it, not others beside them."""
+    ad, x, ids, base = make(tokens, 100, 256, rank, 4, dtype, dtype)
+    ids.copy_(torch.arange(tokens) % 5 - 1)
+    want = mx.mx_lora(x, ad, ids, base)
+    ad.a[1, 3, 7], ad.b[2, :, 1] = float("nan"), float("inf")
+    ad.scales[3] = float("nan")
+    y = mx.mx_lora(x, ad, ids, base)
+    clean = (ids <= 0).nonzero().squeeze(1)
+    assert torch.equal(y[clean], want[clean])
+    assert y[ids == 1].isnan().all() and not y[ids == 2].isfinite().any() and y[ids == 3].isnan().all()
+
+
 def test_huge_and_tiny_values():
     """Rank values far from one keep their bits in the three parts."""
     ad, x, ids, base = make(9, 64, 128, 16, 2, BF16, None)
