@@ -378,7 +378,6 @@ __global__ __launch_bounds__(64 * UW) void k_lora_up(LoraParams p) {
 template <bool F32, int RT>
 hipError_t down(const LoraParams& p, hipStream_t s) {
     const int64_t n = (p.tokens + TOK - 1) / TOK * p.rank_groups * p.spread * p.splits;
-    if (!grid_ok(n, 64 * SW)) return TOO_LARGE;
     k_lora_down<F32, RT><<<(unsigned)n, 64 * SW, 0, s>>>(p);
     return hipGetLastError();
 }
@@ -399,6 +398,11 @@ hipError_t up_rank(const LoraParams& p, hipStream_t s) {
 template <bool F32>
 hipError_t both(LoraParams p, hipStream_t s) {
     p.rank_groups = (p.rank + 63) / 64;
+    // both grids, before either is launched
+    const int64_t tiles = (p.tokens + TOK - 1) / TOK, wide = 16 * UW * (p.tokens <= TOK ? 1 : 4);
+    if (!grid_ok(tiles * p.rank_groups * p.spread * p.splits, 64 * SW) ||
+        !grid_ok((p.n + wide - 1) / wide * ((tiles + p.run - 1) / p.run), 64 * UW))
+        return TOO_LARGE;
     const hipError_t e = p.rank <= 16 ? down<F32, 1>(p, s) : p.rank <= 32 ? down<F32, 2>(p, s) : down<F32, 4>(p, s);
     if (e != hipSuccess) return e;
     return p.tokens <= TOK ? up_rank<F32, 1>(p, s) : up_rank<F32, 4>(p, s);
