@@ -38,6 +38,10 @@ constexpr int tile_tokens(int waves, int rw) { return 32 * waves / rw; }
 constexpr int TABLE = 1024;
 // Tokens that a range of the prefix is a multiple of
 constexpr int UT = 64;
+// Maxima beyond this take the score's product with the scale rounded on its own:
+// a product that is not, less a maximum that was, is off by half the maximum's
+// unit, 2^-4 here and past what 2^x holds from 2^31 on.
+constexpr float FAR = 0x1p20f;
 // LDS row strides in bytes.  Keys: 8 lanes of a 16-byte read take 8 rows, whose
 // starts are then 4 banks apart or a multiple of it, all different.  Values: the
 // transposing read takes 64 bytes of 4 rows, a quarter of the banks each.
@@ -191,6 +195,7 @@ __global__ __launch_bounds__(64 * waves_of(D, QF32, ONE), waves_of(D, QF32, ONE)
 #pragma unroll
         for (int e = 0; e < 16; e++) acc[i][e] = 0.f;
     float m = -INFINITY, l = 0.f;                                  // of row c; l: this lane's tokens
+    bool far = false;                                              // some row's maximum lies beyond FAR
     uint32_t pw[PP][2][4];                                         // probabilities as bf16 pairs
     const int tk = 32 * tw;                                        // this wave's tokens in the tile
 
@@ -246,18 +251,25 @@ __global__ __launch_bounds__(64 * waves_of(D, QF32, ONE), waves_of(D, QF32, ONE)
             const float mn = fmaxf(m, zmax);
             const float grow = __builtin_amdgcn_exp2f(m - (mn == -INFINITY ? 0.f : mn));
             m = mn;
+            far = __any(m != -INFINITY && __builtin_fabsf(m) > FAR);
             l *= grow;
 #pragma unroll
             for (int i = 0; i < D / 32; i++) acc[i] *= grow;
         }
+        if (far) {
+            const float ms = m == -INFINITY ? 0.f : m;
+#pragma unroll
+            for (int e = 0; e < 16; e++) y[e] = y[e] * zs - ms;
+        }
     };
     auto softmax = [&](auto bc) {
         const f16v& y = z[bc.value];
-        const float ms = m == -INFINITY ? 0.f : m;                 // every score so far is -inf
+        const float by = far ? 1.f : zs;
+        const float ms = far || m == -INFINITY ? 0.f : m;          // -inf: every score so far is
 #pragma unroll
         for (int i = 0; i < 8; i++) {
-            float u = __builtin_amdgcn_exp2f(__builtin_fmaf(y[2 * i], zs, -ms));
-            float v = __builtin_amdgcn_exp2f(__builtin_fmaf(y[2 * i + 1], zs, -ms));
+            float u = __builtin_amdgcn_exp2f(__builtin_fmaf(y[2 * i], by, -ms));
+            float v = __builtin_amdgcn_exp2f(__builtin_fmaf(y[2 * i + 1], by, -ms));
             l += u + v;
 #pragma unroll
             for (int k = 0; k < PP; k++) {
