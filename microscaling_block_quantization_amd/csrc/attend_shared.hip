@@ -245,10 +245,11 @@ __global__ __launch_bounds__(64 * waves_of(D, QF32, ONE), waves_of(D, QF32, ONE)
         // the other half's of the same row, without LDS
         const auto both = __builtin_amdgcn_permlane32_swap(fbits(zmax), fbits(zmax), false, false);
         zmax = fmaxf(bitsf(both[0]), bitsf(both[1])) * zs;
-        // Any number near the maximum does for m: it follows only where a row's
-        // maximum has outgrown it by 2^8, seldom after the first tile.
-        if (__any(zmax > m + 8.f)) {
-            const float mn = fmaxf(m, zmax);
+        // Any number from the maximum up to a little more does for m, so that no
+        // probability is above 1: it keeps 2^8 ahead, and follows where a row's
+        // maximum has outgrown it, seldom after the first tile.
+        if (__any(zmax > m)) {
+            const float mn = fmaxf(m, zmax + 8.f);
             const float grow = __builtin_amdgcn_exp2f(m - (mn == -INFINITY ? 0.f : mn));
             m = mn;
             far = __any(m != -INFINITY && __builtin_fabsf(m) > FAR);

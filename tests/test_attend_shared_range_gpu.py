@@ -163,3 +163,38 @@ def test_huge_scores(kind, hk, batch, group, prefix, dim, dtype):
             room = (prefix + 64 + dim + 100) * U * (1 + zu.abs().amax(-1))
             off = ((lse.double() - torch.logsumexp(zu, -1)).abs() / room)[usual].max().item()
             assert off <= 1, f"2^{e} x {scale}: the others' lse at {off:.1f} of the tolerance"
+
+
+@pytest.mark.parametrize("kind", FORMATS)
+@pytest.mark.parametrize("hk,batch,group,prefix", FORMS[1:])
+@pytest.mark.parametrize("dim,dtype", [(64, BF16), (128, BF16), (128, F32), (256, BF16)])
+def test_values_near_the_largest(kind, hk, batch, group, prefix, dim, dtype):
+    """A later token 2^1 to 2^12 times as likely as those before it, with a value
+    near fp32's largest: the weighted sum is finite, and comes out so."""
+    print(kind, hk, batch, group, prefix, dim, dtype, flush=True)
+    kv = torch.zeros(prefix, 2 * hk, dim, device="cuda", dtype=BF16)
+    g = torch.Generator(device="cuda").manual_seed(prefix)
+    heads = torch.arange(hk, device="cuda")
+    late = torch.randint(0, prefix, (hk,), generator=g, device="cuda")
+    kv[late, heads, 0] = 1.0
+    kv[late, hk + heads] = 1.5 * 2.0 ** 126
+    made = Batch(kind, kv, kv.new_zeros(batch, 0, 2 * hk, dim), [0] * batch, 16)
+    q = torch.zeros(batch, hk * group, dim, device="cuda", dtype=dtype)
+    q[:, :, 0] = torch.arange(batch * hk * group, device="cuda").view(batch, -1) % 12 + 1
+    out, lse = made.run(q, math.log(2.0))
+    made.check(q, math.log(2.0), out, lse)
+
+
+@pytest.mark.parametrize("kind", FORMATS)
+@pytest.mark.parametrize("dim,dtype", [(64, BF16), (128, F32)])
+def test_values_near_the_smallest(kind, dim, dtype):
+    """Equal values of 1.5 x 2^-120: what a probability below 2^-6 leaves of one
+    is subnormal and counts."""
+    hk, batch, group, prefix = FORMS[2]
+    g = torch.Generator(device="cuda").manual_seed(prefix)
+    kv = torch.randn(prefix, 2 * hk, dim, generator=g, device="cuda").to(BF16)
+    kv[:, hk:] = 1.5 * 2.0 ** -120
+    made = Batch(kind, kv, kv.new_zeros(batch, 0, 2 * hk, dim), [0] * batch, 16)
+    q = torch.randn(batch, hk * group, dim, generator=g, device="cuda").to(dtype)
+    out, lse = made.run(q, dim ** -0.5)
+    made.check(q, dim ** -0.5, out, lse)
