@@ -198,3 +198,49 @@ def test_values_near_the_smallest(kind, dim, dtype):
     q = torch.randn(batch, hk * group, dim, generator=g, device="cuda").to(dtype)
     out, lse = made.run(q, dim ** -0.5)
     made.check(q, dim ** -0.5, out, lse)
+
+
+# (key-value heads, batch, group): 64, 128 and 256 rows to a tile where the
+# operands allow it, two tiles of rows in the last; ranges of 650 tokens or more
+LONG = [(64, 8, 2), (64, 25, 4), (64, 70, 4)]
+
+
+def long_batch(kind, hk, batch, group, dim, dtype, page, prefix=2651, seed=0):
+    """Scores that climb, fall or jump along the prefix by up to 2^6 each 97
+    tokens, head by head, and heads of scores alike."""
+    g = torch.Generator(device="cuda").manual_seed(seed + dim + batch)
+    kv = torch.randn(prefix, 2 * hk, dim, generator=g, device="cuda")
+    step = torch.arange(prefix, device="cuda") // 97
+    jumps = torch.randperm(int(step[-1]) + 1, generator=g, device="cuda")
+    courses = torch.stack((step, step[-1] - step, jumps[step], 0 * step)).float() * 3
+    kv[:, :hk, 0] = courses[torch.arange(hk, device="cuda") % 4].t()
+    own = torch.randn(batch, 20, 2 * hk, dim, generator=g, device="cuda")
+    lengths = torch.randint(0, 21, (batch,), generator=g, device="cuda").tolist()
+    q = torch.randn(batch, hk * group, dim, generator=g, device="cuda")
+    q[:, :, 0] = 2 + 4 * torch.rand(batch, hk * group, generator=g, device="cuda")
+    return Batch(kind, kv.to(BF16), own.to(BF16), lengths, page), q.to(dtype)
+
+
+@pytest.mark.parametrize("kind", FORMATS)
+@pytest.mark.parametrize("hk,batch,group", LONG)
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("dim", [64, 96, 128, 192, 256])
+def test_long_ranges(kind, hk, batch, group, dtype, dim):
+    """Ranges of five to dozens of tiles, odd and even counts, a ragged end: the
+    maximum moves often, what was summed before is scaled down and counts."""
+    print(kind, hk, batch, group, dtype, dim, flush=True)
+    made, q = long_batch(kind, hk, batch, group, dim, dtype, 16)
+    out, lse = made.run(q, 0.25)
+    made.check(q, 0.25, out, lse)
+
+
+@pytest.mark.parametrize("kind", FORMATS)
+@pytest.mark.parametrize("hk,batch,group", LONG)
+@pytest.mark.parametrize("dim,dtype", [(64, BF16), (128, F32), (256, BF16)])
+@pytest.mark.parametrize("page", [1, 3])
+def test_more_pages_than_are_held(kind, hk, batch, group, dim, dtype, page):
+    """Ranges of more pages than a workgroup holds at a time, refilled between tiles."""
+    print(kind, hk, batch, group, dim, dtype, page, flush=True)
+    made, q = long_batch(kind, hk, batch, group, dim, dtype, page, prefix=4500 * page + 7)
+    out, lse = made.run(q, 0.25)
+    made.check(q, 0.25, out, lse)
