@@ -474,7 +474,9 @@ int mx_cache_read(const mx_kv_cache *cache, const int64_t *slots, int64_t tokens
  *    lengths[b] <= 0: the prefix alone.  Neither: out 0, lse -inf.  A page
  *    outside the cache among the prefix's makes every sequence's outputs NaN.
  *  - Everything else, rounding and order included, as mx_attend; the two agree
- *    up to the order of sums in fp32.  workspace: at least
+ *    up to the order of sums in fp32, and but for tokens of the prefix of less
+ *    than 2^-122 of the likeliest's probability (mx_attend: 2^-126), which
+ *    count as 0.  workspace: at least
  *    mx_attend_shared_workspace_size bytes for this batch and these columns,
  *    which serves every smaller call over a cache of the same form.          */
 size_t mx_attend_shared_workspace_size(const mx_kv_cache *cache, int64_t batch, int32_t q_heads,

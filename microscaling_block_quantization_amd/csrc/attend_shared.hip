@@ -246,10 +246,12 @@ __global__ __launch_bounds__(64 * waves_of(D, QF32, ONE), waves_of(D, QF32, ONE)
         const auto both = __builtin_amdgcn_permlane32_swap(fbits(zmax), fbits(zmax), false, false);
         zmax = fmaxf(bitsf(both[0]), bitsf(both[1])) * zs;
         // Any number from the maximum up to a little more does for m, so that no
-        // probability is above 1: it keeps 2^8 ahead, and follows where a row's
-        // maximum has outgrown it, seldom after the first tile.
+        // probability is above 1.  It keeps 2^4 ahead and follows where a row's
+        // maximum has outgrown it, seldom after the first tile (the 63 us are 69
+        // to 71 with none, 63 to 65 with 2^2); what the exponential gives as 0,
+        // below 2^-126, is then below 2^-122 of the likeliest.
         if (__any(zmax > m)) {
-            const float mn = fmaxf(m, zmax + 8.f);
+            const float mn = fmaxf(m, zmax + 4.f);
             const float grow = __builtin_amdgcn_exp2f(m - (mn == -INFINITY ? 0.f : mn));
             m = mn;
             far = __any(m != -INFINITY && __builtin_fabsf(m) > FAR);

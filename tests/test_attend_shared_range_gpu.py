@@ -200,6 +200,38 @@ def test_values_near_the_smallest(kind, dim, dtype):
     made.check(q, dim ** -0.5, out, lse)
 
 
+@pytest.mark.parametrize("kind", FORMATS)
+@pytest.mark.parametrize("hk,batch,group,prefix", FORMS)
+@pytest.mark.parametrize("dim,dtype", [(64, BF16), (128, F32), (256, BF16)])
+def test_tokens_hardly_likely(kind, hk, batch, group, prefix, dim, dtype):
+    """The likeliest token's value is 0: what a token 2^-60 to 2^-121 times as
+    likely adds is the whole output, wherever the two lie.
+
+    One probability of 16 or 24 bits times an exact value, two joins' factors and
+    a division: 16 u, for bf16 2^-16 and half a unit more."""
+    print(kind, hk, batch, group, prefix, dim, dtype, flush=True)
+    g = torch.Generator(device="cuda").manual_seed(prefix)
+    kv = torch.zeros(prefix, 2 * hk, dim, device="cuda", dtype=BF16)
+    heads = torch.arange(hk, device="cuda")
+    first = torch.randint(0, prefix // 2, (hk,), generator=g, device="cuda")
+    second = torch.randint(prefix // 2, prefix, (hk,), generator=g, device="cuda")
+    swap = torch.rand(hk, generator=g, device="cuda") < 0.5
+    top, other = torch.where(swap, first, second), torch.where(swap, second, first)
+    kv[:, :hk, 0] = -4.0                                  # everyone else: 2^-500 or less
+    kv[top, heads, 0], kv[other, heads, 0] = 1.0, 0.0
+    kv[other, hk + heads] = 1.0
+    made = Batch(kind, kv, kv.new_zeros(batch, 0, 2 * hk, dim), [0] * batch, 16)
+    q = torch.zeros(batch, hk * group, dim, device="cuda")
+    q[:, :, 0] = torch.tensor([60.0, 100.0, 110.0, 118.0, 121.0], device="cuda")[torch.arange(batch * hk * group, device="cuda") % 5].view(batch, -1)
+    # log2 e times fp32's ln 2 is off by u, 121 u in the exponent
+    scale = math.log(2.0)
+    out, lse = made.run(q.to(dtype), scale)
+    want = torch.exp2(-q[:, :, :1].double())
+    tol = 16 * U + 2 * U * 121 * math.log(2.0) + (2.0 ** -16 + 2.0 ** -8 if dtype == BF16 else 0)
+    off = ((out.double() - want).abs() / want).max().item()
+    assert off <= tol, f"off by {off / tol:.2f} of the tolerance"
+
+
 # (key-value heads, batch, group): 64, 128 and 256 rows to a tile where the
 # operands allow it, two tiles of rows in the last; ranges of 650 tokens or more
 LONG = [(64, 8, 2), (64, 25, 4), (64, 70, 4)]
