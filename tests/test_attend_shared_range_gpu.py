@@ -95,6 +95,7 @@ class Batch:
         n = k.shape[1] + width
         parts = 2.0 ** -16 if q.dtype == BF16 else U
         tol = (4 * dz + 16 * U * (1 + zm) + parts + 2 * (n + 64) * U)[..., None] * size
+        tol = tol + n * 2.0 ** -122 * v.abs().max()                # tokens that count as 0
         if q.dtype == BF16:
             tol = tol + 2.0 ** -8 * (want.abs() + tol)
         back = lambda t: t.view(hk, b, per, -1).transpose(0, 1).reshape(b, hq, -1)
