@@ -511,7 +511,8 @@ typedef struct mx_adapters {
  *  - Products and sums are fp32 (a x too: bf16 operands enter exactly, and the
  *    rank values enter the second product as exact sums of three bf16 parts,
  *    multiples of 2^-133).  A NaN or Inf in a token's x reaches its y alone,
- *    one in an adapter the tokens that name it.
+ *    one in an adapter the tokens that name it; an Inf in a bf16 b may leave
+ *    NaN there, as it multiplies parts that are 0.
  *  - workspace: at least mx_lora_workspace_size(a, tokens) bytes, which serves
  *    fewer tokens and smaller ranks too; no initial contents needed; calls that
  *    share one must not overlap.  tokens <= 2^24.                             */

@@ -894,7 +894,9 @@ def mx_lora(x, adapters: Adapters, ids, base=None, y=None, out_dtype=None, works
     output, bf16 or fp32, any row stride; None: zero).  x: tokens x K of the
     adapters' dtype; ids: int32 per token, one outside 0 .. count - 1 (-1, say)
     names none.  y: a tokens x N view to write into (base itself included),
-    else a new tensor of out_dtype (default: base's, without one x's)."""
+    else a new tensor of out_dtype (default: base's, without one x's).  x, base
+    and y each start at a multiple of 16 bytes, and so does every row of x (a
+    slice that does not is refused with MxError)."""
     if stream is not None:
         return _on(stream, mx_lora, x, adapters, ids, base, y, out_dtype, workspace)
     a = adapters.a
@@ -955,7 +957,8 @@ def _logits(z, targets, where):
 def mx_logprobs(logits, targets, top=0, workspace=None, stream=None):
     """Log probability of each row's target, with lse and entropy, and the `top`
     (0 .. 64) likeliest alternatives.  logits: tokens x vocabulary, bf16 or fp32,
-    any row stride; -Inf masks a token.  targets: int64 per token, one outside
+    any row stride, the first row at a multiple of 16 bytes (a slice such as
+    logits[1:] of odd rows is refused with MxError); -Inf masks a token.  targets: int64 per token, one outside
     the vocabulary (padding) has log probability 0.  workspace: as
     alloc_logprobs_workspace gives (allocated when None).  Returns (logprob, lse,
     entropy), fp32 per token, and with top also (top_logprobs, top_ids), tokens x
@@ -986,7 +989,8 @@ def mx_logprobs_backward(d_logprob, d_entropy, logits, targets, lse, entropy=Non
     """Gradient of mx_logprobs' logprob and entropy by the logits: d_logprob and
     d_entropy are theirs, fp32 per token (either may be None), lse and entropy
     its results.  d_logits: a tensor of the logits' shape and dtype to write into
-    (the logits themselves included), else a new one.  Returns d_logits."""
+    (the logits themselves included), else a new one; logits and d_logits start
+    at a multiple of 16 bytes.  Returns d_logits."""
     if stream is not None:
         return _on(stream, mx_logprobs_backward, d_logprob, d_entropy, logits, targets, lse, entropy, d_logits)
     dev = logits.get_device()

@@ -13,12 +13,15 @@
 // 4 sequences behind 65536 bf16 tokens 61 us in all, 4.4 TB/s of cache.  Many:
 // issue slots, most of them the vector unit's (softmax, conversion of cached
 // values to bf16, two bf16 parts of every probability).  64 sequences behind 32768
-// MXFP8 tokens: 63 us for the prefix, 830 TFLOP/s of matrix instructions, of
-// which the second part of the probabilities takes 11 (one part: 52 us; it would
-// double the squared error against 64 bits, so it stays).  Tried there: 4 waves
-// to a workgroup, two of those on a CU, one copy of each tile and two barriers a
-// step 66 us; two groups of waves half a period apart 72 to 80; instruction order
-// by scheduling groups within 1 us of the compiler's.
+// MXFP8 tokens: 63 us for the prefix (fp32 queries, three parts of both: 123), 830
+// TFLOP/s of matrix instructions, of which the second part of the probabilities
+// takes 11 (one part: 52 us; it would double the squared error against 64 bits,
+// so it stays).  Of 148 thousand cycles a SIMD's matrix unit works 50 and its
+// vector unit 53; a wave waits 37 % of its time for issue and 32 % for loads, LDS
+// or a barrier.  Tried there: 4 waves to a workgroup, two of those on a CU, one
+// copy of each tile and two barriers a step 66 us; two groups of waves half a
+// period apart 72 to 80; instruction order by scheduling groups within 1 us of
+// the compiler's.
 #include "attend_device.hpp"
 
 namespace mxk {
@@ -590,6 +593,9 @@ constexpr int FULL = 256;              // workgroups that fill the chip: one for
 // cache lacks registers: 4 sequences (16 rows) behind 65536 tokens take 53 us so
 // and 61 in tiles of 128 rows from MXFP8, 49 and 60 from MXFP4, but 63 and 61
 // from bf16.  A prefix that 64-token ranges cover takes those.
+// Ranges are whole, so where the tiles do not divide 256 some CUs stand idle: 8
+// key-value heads of 256, 16 query heads each, 8192 bf16 tokens take 245 us for 96
+// sequences (192 workgroups), 252 for 128 (256), 475 for 136 (136), 493 for 256.
 SharedPlan shared_plan(const KvCache& c, int64_t batch, int q_heads, int64_t prefix_cols, bool q_bf16) {
     const int64_t rows = batch * (q_heads / c.heads), units = (prefix_cols * c.page + UT - 1) / UT;
     SharedPlan o;

@@ -19,7 +19,16 @@
 // for the join, one round of workgroups whose load, exponentials, bisection and
 // ranking follow each other.  Segments of 32 KB there 26 us, bisection over all
 // integers instead of the lanes' range 15.2; the join by ranking every key 6.5,
-// by bisection 8.8, by binary search in the splits' lists 14.5.
+// by bisection 8.8, by binary search in the splits' lists 14.5.  Without
+// alternatives 4096 x 131072 bf16 takes 221 us, 4.9 TB/s, and 333 x 50001 fp32
+// 15.9 and 3.9 for the join.
+//
+// Rounding.  An exponential's argument is one fp32 product with log2 e, a
+// logarithm the hardware's times ln 2.  Against 64 bits (rms, of 64 x 131072 bf16
+// and 333 x 50001 fp32) log p is off by 5 10^-8 of itself and the entropy by 6.6
+// 10^-8; the elementary form in fp32 by 15 and 5.6.  Carrying the product's error
+// along takes the entropy's from 5.7 to 4.4 in bf16, not at all in fp32, and the
+// 14.2 us to 19.8; the last sums and logarithm in 64 bits leave it within a tenth.
 #include "decode_kernels.hpp"
 
 namespace mxk {
